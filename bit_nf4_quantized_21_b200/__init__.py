@@ -11,6 +11,9 @@ from .qlora import (  # noqa: F401
     qlora_nf4_sizes, qlora_quantize_nf4, qlora_workspace_bytes, status_string,
     qlora_workspace_bytes_dropout, qlora_lora_dropout_mask, qlora_linear_fwd_dropout, qlora_linear_bwd_dropout,
     qlora_paged_alloc, qlora_paged_free, qlora_paged_prefetch,
+    FP8Matrix, empty_fp8, qlora_fp8_sizes, qlora_fp8_quantize, qlora_fp8_linear_fwd, qlora_fp8_linear_bwd,
+    qlora_layernorm_workspace_bytes, qlora_layernorm_fwd, qlora_layernorm_bwd,
+    qlora_distill_topk_fwd, qlora_distill_topk_bwd,
 )
 
 __version__ = "0.1.0"

@@ -1,0 +1,573 @@
+// fp8_linear.cuh -- the frozen linear layer over a weight held in 8-bit
+// floating point (E4M3) with one fp32 scale for each block of 128 x 128, the
+// activations quantised on the way in with one scale for each 1 x 128.
+//
+//   quantiser: s = fp32(absmax / 448), r = fp32(1 / s), q = E4M3_rne(fp32(x r))
+//   forward:   Y[m, n]  = sum over blocks kb of sx[m, kb] sw[n/128, kb] D_kb[m, n],
+//              D_kb[m, n] = sum over k in block kb of qx[m, k] qw[n, k]
+//   dX:        the same with the contraction over n: dX[m, k] = sum over
+//              blocks nb of sg[m, nb] sw[nb, k/128] sum over n in nb of qg[m, n] qw[n, k]
+//
+// Products of E4M3 values are exact in the tensor core's fp32 accumulator;
+// each block's sum is scaled and added in fp32; the output is rounded once.
+//
+// k_fp8_gemm (many tokens), tensor bound.  A pair of SMs (tcgen05.mma
+// cta_group::2, kind::f8f6f4, M 256 x N 256 x K 32) owns a 256 x 256 output
+// tile; each CTA brings its 128 activation rows and its 128-row half of the
+// weight tile by TMA, 32 KB per block of 128 in a ring of six.  A block's
+// product cannot stay in the tensor core's accumulator (the scales differ
+// from block to block), so each block goes into one of two 256-column
+// accumulators in turn, and eight warps take a finished one out while the
+// next is being computed: acc = fma(D, sx sw, acc) in registers, a row of
+// 128 outputs per thread (sx and sw are one number per thread and block).
+// 256 rows x 256 columns keep that work (one multiply-add per 128 products,
+// packed in pairs) and the operand traffic (64 bytes per clock and SM at the
+// full tensor rate) below the tensor time.  The grid is one pair per two
+// SMs and walks the tiles, so that a tile's output is written while the next
+// one's products are already running.  The same weight bytes serve both
+// directions: a tile of 128 rows x 128 bytes is a K-major operand forward
+// and an MN-major one in dX.
+//
+// k_fp8_gemv (few tokens, forward), HBM bound: the weight streams once from
+// global memory straight into the registers of legacy warp-level MMAs
+// (m16n8k32; 16 weight rows x 8 tokens), without shared memory or tensor
+// memory in the way: at M <= 32 the tensor work is 1/100 of what the stream
+// takes, and a warp's fragment loads are whole 64-byte pieces of its rows.
+// Eight warps share a tile's contraction and add their sums in a fixed order.
+#pragma once
+#include <cuda_bf16.h>
+#include <cstdint>
+#include "ptx.cuh"
+
+namespace qlora {
+
+constexpr int kF8Block = 128;
+constexpr float kF8Max = 448.0f;
+
+// ------------------------------------------------------------- quantiser
+// E4M3 codes of (lo, hi), round to nearest even, saturating; NaN stays NaN
+__device__ __forceinline__ uint32_t f8_pack2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint2 f8_pack8(const float (&f)[8], float r) {
+  return make_uint2(f8_pack2(f[0] * r, f[1] * r) | (f8_pack2(f[2] * r, f[3] * r) << 16),
+                    f8_pack2(f[4] * r, f[5] * r) | (f8_pack2(f[6] * r, f[7] * r) << 16));
+}
+// scale and reciprocal of a block; a scale below the smallest normal number
+// stands for a block of zeros
+__device__ __forceinline__ void f8_scale(float absmax, float& s, float& r) {
+  s = __fdiv_rn(absmax, kF8Max);
+  r = 0.0f;
+  if (s < 1.17549435e-38f) s = 0.0f; else r = __frcp_rn(s);
+}
+
+struct Fp8QuantArgs {
+  const void* x;
+  int64_t ldx, rows, cols;
+  uint8_t* codes;
+  int64_t ldq;
+  float* scale;
+  int vec;              // 16-byte loads are aligned for every row
+  int* status;
+};
+
+// elements [c, c + 8) of a row, zeros past its end
+template <typename T>
+__device__ __forceinline__ void f8_load8(const T* row, int64_t c, int64_t cols, int vec, float (&f)[8]) {
+  if (vec && c + 8 <= cols) {
+    if (sizeof(T) == 2) {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + c);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+      }
+    } else {
+      const float4 a = reinterpret_cast<const float4*>(row + c)[0], b = reinterpret_cast<const float4*>(row + c)[1];
+      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? static_cast<float>(row[c + i]) : 0.0f;
+  }
+}
+
+// Blocks of 1 x 128: sixteen lanes per block, eight elements each.  HBM
+// bound (reads 2 or 4 bytes, writes 1 per element).  Scales go out
+// block-major ([cols / 128][rows]), the order in which the GEMM's warps, a
+// row per lane, read them.
+constexpr int kF8QuantThreads = 256;
+template <typename T>
+__global__ void __launch_bounds__(kF8QuantThreads) k_fp8_quant_rows(const Fp8QuantArgs a) {
+  const int64_t blocks = (a.cols + kF8Block - 1) / kF8Block;
+  const int64_t g = (static_cast<int64_t>(blockIdx.x) * kF8QuantThreads + threadIdx.x) >> 4;
+  if (g < a.rows * blocks) {
+    const int64_t row = g / blocks, kb = g % blocks;
+    const int64_t c = kb * kF8Block + (threadIdx.x & 15) * 8;
+    float f[8];
+    f8_load8(static_cast<const T*>(a.x) + row * a.ldx, c, a.cols, a.vec, f);
+    float m = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) { m = fmaxf(m, fabsf(f[i])); bad |= !isfinite(f[i]); }
+    const uint32_t half = 0xFFFFu << (threadIdx.x & 16);   // the other half-warp's block may lie past the end
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, o));
+    float s, r;
+    f8_scale(m, s, r);
+    if (c < a.cols) *reinterpret_cast<uint2*>(a.codes + row * a.ldq + c) = f8_pack8(f, r);
+    if ((threadIdx.x & 15) == 0) a.scale[kb * a.rows + row] = s;
+    if (bad && a.status) atomicOr(a.status, QLORA_DEV_NONFINITE);
+  }
+}
+
+// Blocks of 128 x 128: one CTA per block, 64 elements per thread in registers.
+template <typename T>
+__global__ void __launch_bounds__(256) k_fp8_quant_blocks(const Fp8QuantArgs a) {
+  __shared__ float red[8];
+  const int64_t nkb = (a.cols + kF8Block - 1) / kF8Block;
+  const int64_t nb = blockIdx.x / nkb, kb = blockIdx.x % nkb;
+  const int64_t c = kb * kF8Block + (threadIdx.x & 15) * 8;
+  const int64_t r0 = nb * kF8Block + (threadIdx.x >> 4);
+  float f[8][8];
+  float m = 0.0f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = r0 + 16 * i;
+    if (row < a.rows) {
+      f8_load8(static_cast<const T*>(a.x) + row * a.ldx, c, a.cols, a.vec, f[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) { m = fmaxf(m, fabsf(f[i][e])); bad |= !isfinite(f[i][e]); }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, red[i]);
+  float s, r;
+  f8_scale(m, s, r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = r0 + 16 * i;
+    if (row < a.rows && c < a.cols) *reinterpret_cast<uint2*>(a.codes + row * a.ldq + c) = f8_pack8(f[i], r);
+  }
+  if (threadIdx.x == 0) a.scale[nb * nkb + kb] = s;
+  if (bad && a.status) atomicOr(a.status, QLORA_DEV_NONFINITE);
+}
+
+// --------------------------------------------------- few tokens: the stream
+struct Fp8GemvArgs {
+  const uint8_t* w;
+  int64_t ldw, N, K;
+  const float* sw;       // [ceil(N/128)][ceil(K/128)]
+  const uint8_t* x;
+  int64_t ldx;
+  int M;
+  const float* sx;       // [ceil(K/128)][M]
+  void* y;
+  int64_t ldy;
+  int y_f32;
+};
+
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 bytes of a row from byte k, zeros from byte `end` on (rows are 16-byte
+// aligned and at least `end` rounded up to 16 long)
+__device__ __forceinline__ uint4 f8_bytes16(const uint8_t* row, int64_t k, int64_t end) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (k < end) {
+    v = *reinterpret_cast<const uint4*>(row + k);
+    if (k + 16 > end) {
+      const int n = static_cast<int>(end - k);     // 1 .. 15 bytes stay
+      auto keep = [n](uint32_t w, int at) {
+        const int b = n - at;
+        return b >= 4 ? w : b <= 0 ? 0u : w & ((1u << (8 * b)) - 1u);
+      };
+      v.x = keep(v.x, 0); v.y = keep(v.y, 4); v.z = keep(v.z, 8); v.w = keep(v.w, 12);
+    }
+  }
+  return v;
+}
+
+constexpr int kF8GemvWarps = 8;
+constexpr int kF8GemvRows = 16;
+
+// The contraction's order inside a block is free as long as both operands
+// follow it: lane quad c holds bytes 16c .. 16c + 15 and 64 + 16c .. of each
+// of its rows, and MMA i takes 8 of them.
+template <int NT>
+__global__ void __launch_bounds__(kF8GemvWarps * 32) k_fp8_gemv(const Fp8GemvArgs a) {
+  __shared__ float part[kF8GemvWarps][kF8GemvRows][NT * 8 + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kF8GemvRows;
+  const int64_t blocks = (a.K + kF8Block - 1) / kF8Block;
+  const uint8_t* w0 = a.w + min(n0 + g, a.N - 1) * a.ldw;
+  const uint8_t* w1 = a.w + min(n0 + g + 8, a.N - 1) * a.ldw;
+  const float* sw = a.sw + (n0 / kF8Block) * blocks;
+  float acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
+
+  uint4 next[4];
+  float nsw = 0.0f;
+  auto fetch = [&](int64_t kb) {
+    const int64_t k = kb * kF8Block + 16 * c;
+    next[0] = f8_bytes16(w0, k, a.K);
+    next[1] = f8_bytes16(w1, k, a.K);
+    next[2] = f8_bytes16(w0, k + 64, a.K);
+    next[3] = f8_bytes16(w1, k + 64, a.K);
+    nsw = sw[kb];
+  };
+  if (warp < blocks) fetch(warp);
+  for (int64_t kb = warp; kb < blocks; kb += kF8GemvWarps) {
+    const uint4 p0 = next[0], q0 = next[1], p1 = next[2], q1 = next[3];
+    const float s = nsw;
+    if (kb + kF8GemvWarps < blocks) fetch(kb + kF8GemvWarps);
+    const int64_t k = kb * kF8Block + 16 * c;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int tok = t * 8 + g;
+      uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+      if (tok < a.M) {
+        x0 = f8_bytes16(a.x + tok * a.ldx, k, a.K);
+        x1 = f8_bytes16(a.x + tok * a.ldx, k + 64, a.K);
+      }
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      mma_e4m3(d, p0.x, q0.x, p0.y, q0.y, x0.x, x0.y);
+      mma_e4m3(d, p0.z, q0.z, p0.w, q0.w, x0.z, x0.w);
+      mma_e4m3(d, p1.x, q1.x, p1.y, q1.y, x1.x, x1.y);
+      mma_e4m3(d, p1.z, q1.z, p1.w, q1.w, x1.z, x1.w);
+      const int t0 = t * 8 + 2 * c;
+      const float s0 = t0 < a.M ? s * a.sx[kb * a.M + t0] : 0.0f;
+      const float s1 = t0 + 1 < a.M ? s * a.sx[kb * a.M + t0 + 1] : 0.0f;
+      acc[t][0] = fmaf(d[0], s0, acc[t][0]);
+      acc[t][1] = fmaf(d[1], s1, acc[t][1]);
+      acc[t][2] = fmaf(d[2], s0, acc[t][2]);
+      acc[t][3] = fmaf(d[3], s1, acc[t][3]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    part[warp][g][t * 8 + 2 * c] = acc[t][0];
+    part[warp][g][t * 8 + 2 * c + 1] = acc[t][1];
+    part[warp][g + 8][t * 8 + 2 * c] = acc[t][2];
+    part[warp][g + 8][t * 8 + 2 * c + 1] = acc[t][3];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kF8GemvRows * NT * 8; i += kF8GemvWarps * 32) {
+    const int r = i % kF8GemvRows, tok = i / kF8GemvRows;
+    if (tok < a.M && n0 + r < a.N) {
+      float s = part[0][r][tok];
+#pragma unroll
+      for (int k = 1; k < kF8GemvWarps; ++k) s += part[k][r][tok];
+      const int64_t at = tok * a.ldy + n0 + r;
+      if (a.y_f32) static_cast<float*>(a.y)[at] = s;
+      else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(s);
+    }
+  }
+}
+
+// ---------------------------------------------- many tokens: the 2-SM GEMM
+constexpr int kF8Ring = 6;
+constexpr int kF8EpiWarps = 8;
+constexpr int kF8ProdWarp = 8;
+constexpr int kF8IssueWarp = 9;                  // and 10: two issuers
+constexpr int kF8Threads = 32 * 11;
+constexpr uint32_t kF8OpBytes = 128 * 128;       // 16 KB: 128 rows x 128 bytes
+constexpr uint32_t kF8SlotBytes = 2 * kF8OpBytes;
+constexpr uint32_t kF8SmemBytes = kF8Ring * kF8SlotBytes + 1024 /*align*/ + 256 /*bars*/;
+constexpr uint32_t kF8TmemCols = 512;
+constexpr int kF8GroupM = 8;
+static_assert(kF8Ring % 2 == 0, "each slot belongs to one issuer");
+static_assert(kF8SmemBytes <= 227 * 1024, "fp8 GEMM shared memory");
+
+struct Fp8GemmArgs {
+  int64_t M;             // activation rows
+  int64_t out_cols;      // N (forward) or K (dX)
+  int64_t ctr;           // contraction length
+  const float* sa;       // activation scales [ceil(ctr/128)][M]
+  const float* sw;       // weight scales [ceil(N/128)][ceil(K/128)]
+  int64_t sw_cols;       // ceil(K/128)
+  void* out;
+  int64_t ldo;
+  int out_f32;
+  int out_vec;           // 16-byte stores are aligned for every row
+  int tiles_m, tiles_n;
+  int* status;
+};
+
+// D[tmem] (+)= A[smem] * B[smem]^T over a 2-SM pair, E4M3 x E4M3 -> fp32, K = 32
+__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor, kind::f8f6f4: E4M3 x E4M3 (format 0) -> fp32
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int b_mn_major) {
+  return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+// arrive on the barrier of another CTA of the cluster, ordering this
+// thread's earlier accesses before it at cluster scope
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// bounded wait with acquire at cluster scope
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  uint32_t spins = 0;
+  while (true) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((++spins & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (global_ns() - t0 > qlora_wait_limit()) {
+        *abort_flag = 1;
+        if (status) atomicOr(status, QLORA_DEV_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// output tile t: groups of kF8GroupM tile rows, a group's columns one after
+// the other, so that the tiles in flight share rows and columns in L2
+__device__ __forceinline__ void f8_tile(int t, const Fp8GemmArgs& a, int& tm, int& tn) {
+  const int per = kF8GroupM * a.tiles_n;
+  const int g = t / per, r = t % per;
+  const int h = min(kF8GroupM, a.tiles_m - g * kF8GroupM);
+  tm = g * kF8GroupM + r % h;
+  tn = r / h;
+}
+
+// MODE 0: forward (weight tile K-major), 1: dX (weight tile MN-major)
+template <int MODE>
+__global__ void __launch_bounds__(kF8Threads, 1)
+    k_fp8_gemm(const __grid_constant__ CUtensorMap tm_act, const __grid_constant__ CUtensorMap tm_w,
+               const Fp8GemmArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kF8Ring * kF8SlotBytes);
+  uint64_t* full = bars;                         // [ring] leader: both CTAs' tiles landed
+  uint64_t* empty = full + kF8Ring;              // [ring] local: MMA done with the slot
+  uint64_t* acc_full = empty + kF8Ring;          // [2] local: accumulator holds a block's product
+  uint64_t* acc_empty = acc_full + 2;            // [2] leader: both CTAs have taken it out
+  uint64_t* drained = acc_empty + 2;             // local: every MMA issued is done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+  const int tiles = args.tiles_m * args.tiles_n;
+  const int KB = static_cast<int>((args.ctr + kF8Block - 1) / kF8Block);
+  const int mine = pair < tiles ? (tiles - pair + pairs - 1) / pairs : 0;   // this pair's tiles
+  const int64_t total = static_cast<int64_t>(mine) * KB;                   // blocks over all of them
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kF8Ring; ++i) { mbar_init(smem_u32(&full[i]), 1); mbar_init(smem_u32(&empty[i]), 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&acc_full[i]), 1);
+      mbar_init(smem_u32(&acc_empty[i]), 2 * kF8EpiWarps);
+    }
+    mbar_init(smem_u32(drained), 2);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kF8ProdWarp) {
+    if (lane == 0) { tma_prefetch_desc(&tm_act); tma_prefetch_desc(&tm_w); }
+    __syncwarp();
+    tmem_alloc_pair(smem_u32(tmem_slot), kF8TmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();   // both CTAs' barriers initialised before any cross-CTA use
+  tc_fence_after();
+  const uint32_t tmem_d = *tmem_slot;
+  auto leader_bar = [&](uint64_t* b) { return mapa_shared(smem_u32(b), 0); };
+  if (threadIdx.x == 0) QLORA_CHECK_ONLY(kF8SmemBytes <= dyn_smem_bytes(), 200);
+
+  if (warp == kF8ProdWarp) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int64_t it = 0;
+      bool live = true;
+      for (int t = pair; t < tiles && live; t += pairs) {
+        int tm, tn;
+        f8_tile(t, args, tm, tn);
+        const int32_t m0 = tm * 256 + static_cast<int32_t>(rank) * 128;
+        const int32_t c0 = tn * 256 + static_cast<int32_t>(rank) * 128;   // this CTA's half of the output columns
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int s = static_cast<int>(it % kF8Ring);
+          if (it >= kF8Ring &&
+              !mbar_wait(smem_u32(&empty[s]), static_cast<uint32_t>((it / kF8Ring + 1) & 1), abort_flag, args.status)) {
+            live = false;
+            break;
+          }
+          const uint32_t fb = leader_bar(&full[s]);
+          if (leader) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * kF8SlotBytes);
+          const uint32_t dst = smem_u32(base) + s * kF8SlotBytes;
+          // (a skipped load leaves the slot's wait to run out: bounded, the launch aborts)
+          if (QLORA_CHECK(s >= 0 && (s + 1) * kF8SlotBytes <= kF8Ring * kF8SlotBytes && m0 >= 0 && c0 >= 0, 201)) {
+            tma_load_2d_pair(dst, &tm_act, fb, kb * kF8Block, m0);
+            if (MODE == 0) tma_load_2d_pair(dst + kF8OpBytes, &tm_w, fb, kb * kF8Block, c0);
+            else tma_load_2d_pair(dst + kF8OpBytes, &tm_w, fb, c0, kb * kF8Block);
+          }
+        }
+      }
+      if (*abort_flag && leader) {
+        // loads still in flight land before the CTA can exit
+        for (int64_t i = it > kF8Ring ? it - kF8Ring : 0; i < it; ++i) {
+          const uint64_t t1 = global_ns();
+          while (!mbar_try_wait_cluster(smem_u32(&full[i % kF8Ring]), static_cast<uint32_t>((i / kF8Ring) & 1)) &&
+                 global_ns() - t1 < qlora_drain_limit()) {}
+        }
+      }
+    }
+  } else if (warp >= kF8IssueWarp) {
+    // ------------------------------------------------- MMA issuers (leader)
+    // Issuer i takes blocks i, i + 2, ... into accumulator i: a thread that
+    // waits right after issuing stalls until its MMAs drain, so two take turns.
+    if (leader && lane == 0) {
+      const int me = warp - kF8IssueWarp;
+      constexpr uint32_t idesc = idesc_e4m3(256, 256, MODE);
+      const uint32_t dcol = tmem_d + 256u * me;
+      for (int64_t it = me; it < total; it += 2) {
+        const int s = static_cast<int>(it % kF8Ring);
+        const int64_t use = it >> 1;
+        if (use > 0 && !mbar_wait_cluster(smem_u32(&acc_empty[me]), static_cast<uint32_t>((use + 1) & 1), abort_flag, args.status))
+          break;
+        if (!mbar_wait_cluster(smem_u32(&full[s]), static_cast<uint32_t>((it / kF8Ring) & 1), abort_flag, args.status)) break;
+        tc_fence_after();
+        const uint32_t ab = smem_u32(base) + s * kF8SlotBytes, wb = ab + kF8OpBytes;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t adesc = sw128_desc(ab + k * 32, 16, 1024);
+          const uint64_t bdesc = MODE == 0 ? sw128_desc(wb + k * 32, 16, 1024) : sw128_desc(wb + k * 4096, 16384, 1024);
+          umma_e4m3_pair(dcol, adesc, bdesc, idesc, k > 0 ? 1u : 0u);
+        }
+        umma_commit_pair(smem_u32(&empty[s]), 0x3);
+        umma_commit_pair(smem_u32(&acc_full[me]), 0x3);
+      }
+      umma_commit_pair(smem_u32(drained), 0x3);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    // Warp w: rows 32 (w % 4) .. of this CTA, output columns 128 (w / 4) ..
+    const int q = warp & 3, half = warp >> 2;
+    const uint32_t taddr = tmem_d + (static_cast<uint32_t>(q * 32) << 16) + 128u * half;
+    int64_t it = 0;
+    bool live = true;
+    for (int t = pair; t < tiles && live; t += pairs) {
+      int tm, tn;
+      f8_tile(t, args, tm, tn);
+      const int64_t row = static_cast<int64_t>(tm) * 256 + rank * 128 + q * 32 + lane;
+      const int64_t col = static_cast<int64_t>(tn) * 256 + 128 * half;
+      const bool in = row < args.M && col < args.out_cols;
+      const float* sa = args.sa + (in ? row : 0);
+      const int64_t ob = in ? col / kF8Block : 0;
+      const float* sw = MODE == 0 ? args.sw + ob * args.sw_cols : args.sw + ob;
+      const int64_t sw_step = MODE == 0 ? 1 : args.sw_cols;
+      auto scale_of = [&](int kb) { return kb < KB ? sa[kb * args.M] * sw[kb * sw_step] : 0.0f; };
+      float s0 = scale_of(0), s1 = scale_of(1);
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+      for (int kb = 0; kb < KB; ++kb, ++it) {
+        const int buf = static_cast<int>(it & 1);
+        const float s = s0;
+        s0 = s1;
+        s1 = scale_of(kb + 2);
+        if (!mbar_wait_cluster(smem_u32(&acc_full[buf]), static_cast<uint32_t>((it >> 1) & 1), abort_flag, args.status)) {
+          live = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t r[16];
+          tmem_ld16(taddr + 256u * buf + 16 * c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[16 * c + i] = fmaf(__uint_as_float(r[i]), s, acc[16 * c + i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_release_cluster(leader_bar(&acc_empty[buf]));
+      }
+      if (live && in) {
+        const int64_t left = args.out_cols - col;
+        if (args.out_f32) {
+          float* dst = static_cast<float*>(args.out) + row * args.ldo + col;
+#pragma unroll
+          for (int c = 0; c < 128; c += 4) {
+            if (args.out_vec && c + 4 <= left) {
+              *reinterpret_cast<float4*>(dst + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (c + i < left) dst[c + i] = acc[c + i];
+            }
+          }
+        } else {
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(args.out) + row * args.ldo + col;
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+            if (args.out_vec && c + 8 <= left) {
+              *reinterpret_cast<uint4*>(dst + c) =
+                  make_uint4(pack_bf16x2(acc[c], acc[c + 1]), pack_bf16x2(acc[c + 2], acc[c + 3]),
+                             pack_bf16x2(acc[c + 4], acc[c + 5]), pack_bf16x2(acc[c + 6], acc[c + 7]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (c + i < left) dst[c + i] = __float2bfloat16_rn(acc[c + i]);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // Single-lane roles leave their warps diverged; the cluster barrier is
+  // warp-aligned, and tensor memory must not be released under running MMAs
+  // (on an aborted launch some may be: wait for the issuers' last commit).
+  __syncwarp();
+  if (warp == kF8ProdWarp) {
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait_cluster(smem_u32(drained), 0) && global_ns() - t0 < qlora_wait_limit()) {}
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == kF8ProdWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_d, kF8TmemCols);
+  }
+}
+
+}  // namespace qlora

@@ -1,0 +1,440 @@
+// layernorm.cuh -- layer norm over the last dimension, forward and backward,
+// with the reduction of the weight's and the bias's gradient.
+//
+//   mean = sum x / C        rstd = 1 / sqrt(sum (x - mean)^2 / C + eps)
+//   y  = (x - mean) rstd w + b
+//   xh = (x - mean) rstd    g = dy w
+//   dx = rstd (g - mean(g) - xh mean(g xh))
+//   dw = sum over rows of dy xh        db = sum over rows of dy
+//
+// Every sum is fp32; the variance is the sum of squared differences from
+// the mean (a second sweep over registers), never sum(x^2) - mean^2, which
+// loses everything when the mean is far above the spread.  A row is read
+// from memory once and held in registers between the sweeps; outputs are
+// rounded once.
+//
+// HBM bound: 2 elements moved per element forward, 3 backward.  A group of
+// GROUP threads owns a row (a warp for short rows, so that no block barrier
+// is needed; up to 1024 threads for long ones), each thread PER chunks of
+// VEC elements.  VEC is 16 bytes when the row length, strides and pointers
+// allow it, otherwise one element.  Rows that do not fit the registers take
+// the streaming kernels, which read a row again from L1/L2 per sweep.
+//
+// The backward walks rows with a fixed grid: a thread keeps the same columns
+// for every row, so its share of dw and db accumulates in registers and is
+// written once per group as a row of partials; k_ln_finish adds the partials
+// in a fixed order (no atomics: results do not depend on scheduling).
+#pragma once
+#include <cuda_bf16.h>
+#include <cstdint>
+#include "ptx.cuh"
+
+namespace qlora {
+
+constexpr int kLnMaxParts = 592;     // most partial rows of dw/db that a backward call writes
+
+struct LnArgs {
+  const void* x;
+  int64_t ldx;
+  const void* w;        // nullable: ones
+  const void* b;        // nullable: zeros
+  int w_bf16;
+  int64_t rows, cols;
+  float eps;
+  void* y;              // forward
+  int64_t ldy;
+  float* mean;          // forward: written when non-null; backward: read
+  float* rstd;
+  const void* dy;       // backward
+  int64_t lddy;
+  void* dx;
+  int64_t lddx;
+  float* part;          // [parts][2][cols] partials of dw, db; null: not wanted
+};
+
+template <typename T> struct LnElem;
+template <> struct LnElem<float> { static constexpr int kVec = 4; };
+template <> struct LnElem<__nv_bfloat16> { static constexpr int kVec = 8; };
+
+// VEC consecutive elements as loaded (16 bytes, or one element)
+template <typename T, int VEC> struct LnRaw;
+template <> struct LnRaw<__nv_bfloat16, 8> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <> struct LnRaw<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&f)[4]) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+};
+template <> struct LnRaw<__nv_bfloat16, 1> {
+  __nv_bfloat16 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *p; }
+  __device__ __forceinline__ void zero() { v = __float2bfloat16_rn(0.0f); }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = __bfloat162float(v); }
+};
+template <> struct LnRaw<float, 1> {
+  float v;
+  __device__ __forceinline__ void load(const float* p) { v = *p; }
+  __device__ __forceinline__ void zero() { v = 0.0f; }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = v; }
+};
+
+__device__ __forceinline__ void ln_store(__nv_bfloat16* p, const float (&f)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                            pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ void ln_store(float* p, const float (&f)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void ln_store(__nv_bfloat16* p, const float (&f)[1]) { *p = __float2bfloat16_rn(f[0]); }
+__device__ __forceinline__ void ln_store(float* p, const float (&f)[1]) { *p = f[0]; }
+
+// VEC parameters (weight or bias, bf16 or fp32) from column c; `fill` when absent
+template <int VEC>
+__device__ __forceinline__ void ln_param(const void* p, int bf16, int64_t c, float fill, float (&f)[VEC]) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = fill;
+  } else if (VEC == 1) {
+    f[0] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[c]) : static_cast<const float*>(p)[c];
+  } else if (bf16) {
+    const uint2* q = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + c);
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const uint2 u = q[i];
+      f[4 * i] = __uint_as_float(u.x << 16);
+      f[4 * i + 1] = __uint_as_float(u.x & 0xFFFF0000u);
+      f[4 * i + 2] = __uint_as_float(u.y << 16);
+      f[4 * i + 3] = __uint_as_float(u.y & 0xFFFF0000u);
+    }
+  } else {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const float4 u = q[i];
+      f[4 * i] = u.x; f[4 * i + 1] = u.y; f[4 * i + 2] = u.z; f[4 * i + 3] = u.w;
+    }
+  }
+}
+
+// Sums of two values over a group of GROUP threads, the same in every thread
+// of the group.  `red` holds one float2 per warp; consecutive calls of a
+// block alternate between two such buffers, so one barrier per call is
+// enough (a buffer is written again only after the next call's barrier).
+template <int GROUP>
+__device__ __forceinline__ float2 ln_group_sum(float2 v, float2* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
+    v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
+  }
+  if (GROUP == 32) return v;
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) red[warp] = v;
+  __syncthreads();
+  float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < GROUP / 32; ++i) {
+    const float2 u = red[i];
+    s.x += u.x;
+    s.y += u.y;
+  }
+  return s;
+}
+
+template <int GROUP> constexpr int ln_block() { return GROUP < 128 ? 128 : GROUP; }
+
+template <typename T, int VEC, int GROUP, int PER>
+__global__ void __launch_bounds__(ln_block<GROUP>()) k_ln_fwd(const LnArgs a) {
+  constexpr int kRows = ln_block<GROUP>() / GROUP;
+  __shared__ float2 red[2][32];
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / GROUP;
+  const int t = threadIdx.x % GROUP;
+  if (row >= a.rows) return;            // whole warps only: a group of a warp, or the block's one row
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  LnRaw<T, VEC> raw[PER];
+  float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
+    if (c < a.cols) raw[i].load(x + c); else raw[i].zero();
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    float f[VEC];
+    raw[i].get(f);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s.x += f[e];
+  }
+  const float inv = 1.0f / static_cast<float>(a.cols);
+  const float mean = ln_group_sum<GROUP>(s, red[0]).x * inv;
+  s = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
+    float f[VEC];
+    raw[i].get(f);
+    if (c < a.cols) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float d = f[e] - mean;
+        s.x = fmaf(d, d, s.x);
+      }
+    }
+  }
+  const float rstd = 1.0f / sqrtf(ln_group_sum<GROUP>(s, red[1]).x * inv + a.eps);
+  T* y = static_cast<T*>(a.y) + row * a.ldy;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
+    if (c < a.cols) {
+      float f[VEC], w[VEC], b[VEC];
+      raw[i].get(f);
+      ln_param<VEC>(a.w, a.w_bf16, c, 1.0f, w);
+      ln_param<VEC>(a.b, a.w_bf16, c, 0.0f, b);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[e], b[e]);
+      ln_store(y + c, f);
+    }
+  }
+  if (t == 0) {
+    if (a.mean) a.mean[row] = mean;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+}
+
+// Any row length: a block per row, the row read again per sweep.
+constexpr int kLnStreamThreads = 512;
+template <typename T>
+__global__ void __launch_bounds__(kLnStreamThreads) k_ln_fwd_stream(const LnArgs a) {
+  __shared__ float2 red[2][32];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const float inv = 1.0f / static_cast<float>(a.cols);
+  float2 s = make_float2(0.0f, 0.0f);
+  for (int64_t c = threadIdx.x; c < a.cols; c += kLnStreamThreads) s.x += static_cast<float>(x[c]);
+  const float mean = ln_group_sum<kLnStreamThreads>(s, red[0]).x * inv;
+  s.x = 0.0f;
+  for (int64_t c = threadIdx.x; c < a.cols; c += kLnStreamThreads) {
+    const float d = static_cast<float>(x[c]) - mean;
+    s.x = fmaf(d, d, s.x);
+  }
+  const float rstd = 1.0f / sqrtf(ln_group_sum<kLnStreamThreads>(s, red[1]).x * inv + a.eps);
+  T* y = static_cast<T*>(a.y) + row * a.ldy;
+  for (int64_t c = threadIdx.x; c < a.cols; c += kLnStreamThreads) {
+    float w[1], b[1], f[1];
+    ln_param<1>(a.w, a.w_bf16, c, 1.0f, w);
+    ln_param<1>(a.b, a.w_bf16, c, 0.0f, b);
+    f[0] = fmaf((static_cast<float>(x[c]) - mean) * rstd, w[0], b[0]);
+    ln_store(y + c, f);
+  }
+  if (threadIdx.x == 0) {
+    if (a.mean) a.mean[row] = mean;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+}
+
+// Backward, rows in registers.  The grid walks the rows; the loads of the
+// next row are in flight while the current one is reduced.
+template <typename T, int VEC, int GROUP, int PER>
+__global__ void __launch_bounds__(ln_block<GROUP>()) k_ln_bwd(const LnArgs a) {
+  constexpr int kRows = ln_block<GROUP>() / GROUP;
+  __shared__ float2 red[2][32];
+  const int t = threadIdx.x % GROUP;
+  const int64_t group = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / GROUP;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  float dw[PER][VEC], db[PER][VEC];
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) dw[i][e] = db[i][e] = 0.0f;
+  const float inv = 1.0f / static_cast<float>(a.cols);
+  LnRaw<T, VEC> rx[PER], rd[PER];
+  float mean = 0.0f, rstd = 0.0f;
+  auto fetch = [&](int64_t row) {
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
+      if (c < a.cols) { rx[i].load(x + c); rd[i].load(dy + c); } else { rx[i].zero(); rd[i].zero(); }
+    }
+    mean = a.mean[row];
+    rstd = a.rstd[row];
+  };
+  // a group of a warp ends its loop by itself; a group of a block has one row per block
+  int64_t row = group;
+  if (row < a.rows) fetch(row);
+  int buf = 0;
+  for (; row < a.rows; row += step) {
+    LnRaw<T, VEC> x[PER], d[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) { x[i] = rx[i]; d[i] = rd[i]; }
+    const float mu = mean, rs = rstd;
+    if (row + step < a.rows) fetch(row + step);
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
+      if (c < a.cols) {
+        float fx[VEC], fd[VEC], w[VEC];
+        x[i].get(fx);
+        d[i].get(fd);
+        ln_param<VEC>(a.w, a.w_bf16, c, 1.0f, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float xh = (fx[e] - mu) * rs, g = fd[e] * w[e];
+          s.x += g;
+          s.y = fmaf(g, xh, s.y);
+          dw[i][e] = fmaf(fd[e], xh, dw[i][e]);
+          db[i][e] += fd[e];
+        }
+      }
+    }
+    s = ln_group_sum<GROUP>(s, red[buf]);
+    buf ^= 1;
+    const float m1 = s.x * inv, m2 = s.y * inv;
+    T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
+      if (c < a.cols) {
+        float fx[VEC], fd[VEC], w[VEC], o[VEC];
+        x[i].get(fx);
+        d[i].get(fd);
+        ln_param<VEC>(a.w, a.w_bf16, c, 1.0f, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float xh = (fx[e] - mu) * rs;
+          o[e] = rs * (fmaf(fd[e], w[e], -m1) - xh * m2);
+        }
+        ln_store(dx + c, o);
+      }
+    }
+  }
+  if (a.part) {
+    float* pw = a.part + group * 2 * a.cols;
+    float* pb = pw + a.cols;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
+      if (c < a.cols) {
+        if (VEC == 1) {
+          pw[c] = dw[i][0];
+          pb[c] = db[i][0];
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; e += 4) {
+            *reinterpret_cast<float4*>(pw + c + e) =
+                make_float4(dw[i][e], dw[i][(e + 1) % VEC], dw[i][(e + 2) % VEC], dw[i][(e + 3) % VEC]);
+            *reinterpret_cast<float4*>(pb + c + e) =
+                make_float4(db[i][e], db[i][(e + 1) % VEC], db[i][(e + 2) % VEC], db[i][(e + 3) % VEC]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Any row length: dx with a block per row, then the columns' partials with a
+// thread per column and a run of rows per block row of the grid.
+template <typename T>
+__global__ void __launch_bounds__(kLnStreamThreads) k_ln_bwd_stream(const LnArgs a) {
+  __shared__ float2 red[2][32];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+  const float mu = a.mean[row], rs = a.rstd[row];
+  float2 s = make_float2(0.0f, 0.0f);
+  for (int64_t c = threadIdx.x; c < a.cols; c += kLnStreamThreads) {
+    float w[1];
+    ln_param<1>(a.w, a.w_bf16, c, 1.0f, w);
+    const float g = static_cast<float>(dy[c]) * w[0];
+    s.x += g;
+    s.y = fmaf(g, (static_cast<float>(x[c]) - mu) * rs, s.y);
+  }
+  s = ln_group_sum<kLnStreamThreads>(s, red[0]);
+  const float inv = 1.0f / static_cast<float>(a.cols);
+  const float m1 = s.x * inv, m2 = s.y * inv;
+  T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+  for (int64_t c = threadIdx.x; c < a.cols; c += kLnStreamThreads) {
+    float w[1], o[1];
+    ln_param<1>(a.w, a.w_bf16, c, 1.0f, w);
+    const float xh = (static_cast<float>(x[c]) - mu) * rs;
+    o[0] = rs * (fmaf(static_cast<float>(dy[c]), w[0], -m1) - xh * m2);
+    ln_store(dx + c, o);
+  }
+}
+
+constexpr int kLnColThreads = 128;
+template <typename T>
+__global__ void __launch_bounds__(kLnColThreads) k_ln_bwd_cols(const LnArgs a) {
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kLnColThreads + threadIdx.x;
+  if (c >= a.cols) return;
+  float dw = 0.0f, db = 0.0f;
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const float d = static_cast<float>(static_cast<const T*>(a.dy)[row * a.lddy + c]);
+    const float xh = (static_cast<float>(static_cast<const T*>(a.x)[row * a.ldx + c]) - a.mean[row]) * a.rstd[row];
+    dw = fmaf(d, xh, dw);
+    db += d;
+  }
+  float* pw = a.part + static_cast<int64_t>(blockIdx.y) * 2 * a.cols;
+  pw[c] = dw;
+  pw[a.cols + c] = db;
+}
+
+// dw and db from the partial rows: 32 columns per block, 32 row lanes, the
+// lanes' sums added in a fixed tree.
+struct LnFinishArgs {
+  const float* part;
+  int parts;
+  int64_t cols;
+  void* dw;             // nullable
+  void* db;             // nullable
+  int out_bf16;
+};
+__global__ void __launch_bounds__(1024) k_ln_finish(const LnFinishArgs a) {
+  __shared__ float2 sm[32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + x;
+  float2 s = make_float2(0.0f, 0.0f);
+  if (c < a.cols) {
+    for (int p = y; p < a.parts; p += 32) {
+      const float* q = a.part + static_cast<int64_t>(p) * 2 * a.cols + c;
+      s.x += q[0];
+      s.y += q[a.cols];
+    }
+  }
+  sm[y][x] = s;
+  __syncthreads();
+  // row y of the transposed tile: column y's 32 lane sums in one warp
+  s = sm[x][y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, o);
+    s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, o);
+  }
+  const int64_t oc = static_cast<int64_t>(blockIdx.x) * 32 + y;
+  if (x == 0 && oc < a.cols) {
+    if (a.out_bf16) {
+      if (a.dw) static_cast<__nv_bfloat16*>(a.dw)[oc] = __float2bfloat16_rn(s.x);
+      if (a.db) static_cast<__nv_bfloat16*>(a.db)[oc] = __float2bfloat16_rn(s.y);
+    } else {
+      if (a.dw) static_cast<float*>(a.dw)[oc] = s.x;
+      if (a.db) static_cast<float*>(a.db)[oc] = s.y;
+    }
+  }
+}
+
+}  // namespace qlora

@@ -31,6 +31,9 @@
 #include "adam.cuh"
 #include "merge.cuh"
 #include "dropout.cuh"
+#include "layernorm.cuh"
+#include "distill.cuh"
+#include "fp8_linear.cuh"
 
 using namespace qlora;
 
@@ -116,6 +119,8 @@ bool ensure_smem_attrs() {
   ok = ok && cudaFuncSetAttribute(k_skinny<0, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) == cudaSuccess;
   ok = ok && cudaFuncSetAttribute(k_skinny<1, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) == cudaSuccess;
   ok = ok && cudaFuncSetAttribute(k_gemv_nf4, cudaFuncAttributeMaxDynamicSharedMemorySize, kGvSmemBytes) == cudaSuccess;
+  ok = ok && cudaFuncSetAttribute(k_fp8_gemm<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8SmemBytes) == cudaSuccess;
+  ok = ok && cudaFuncSetAttribute(k_fp8_gemm<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8SmemBytes) == cudaSuccess;
   if (ok) done.fetch_or(bit);
   return ok;
 }
@@ -1263,3 +1268,445 @@ extern "C" qlora_status qlora_linear_fwd_noalloc(const void* X, int64_t M, const
 
   return run_fused(kModeFwd, X, Wq, nullptr, d, sT, Bp, Y, nullptr, d_status, cs);
 }
+
+// ============================================================ FP8 linear layer
+namespace {
+
+bool is_io_dtype(qlora_dtype d) { return d == QLORA_F32 || d == QLORA_BF16; }
+size_t dtype_size(qlora_dtype d) { return d == QLORA_F32 ? 4 : 2; }
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// every row of a strided matrix starts on a 16-byte boundary
+bool rows16(const void* p, int64_t ld, size_t elem) {
+  return aligned16(p) && (static_cast<uint64_t>(ld) * elem) % 16 == 0;
+}
+
+qlora_status check_fp8(const qlora_fp8_matrix* m, int block_rows) {
+  if (!m) return QLORA_ERR_INVALID_ARG;
+  if (m->rows < 0 || m->cols < 1 || m->ld < m->cols || m->ld % 16 != 0) return QLORA_ERR_INVALID_ARG;
+  if (m->reserved != 0 || (m->block_rows != 1 && m->block_rows != kF8Block)) return QLORA_ERR_INVALID_ARG;
+  if (block_rows && m->block_rows != block_rows) return QLORA_ERR_INVALID_ARG;
+  // tile coordinates are 32-bit
+  if (m->rows > (int64_t(1) << 30) || m->ld > (int64_t(1) << 30)) return QLORA_ERR_UNSUPPORTED;
+  if (m->rows == 0) return QLORA_OK;
+  if (!m->codes || !aligned16(m->codes) || !m->scale || !aligned_to(m->scale, 4)) return QLORA_ERR_INVALID_ARG;
+  return QLORA_OK;
+}
+
+qlora_status run_fp8_quantize(const void* X, qlora_dtype dt, int64_t ldx, const qlora_fp8_matrix* out, int* status,
+                              cudaStream_t cs) {
+  Fp8QuantArgs a{};
+  a.x = X; a.ldx = ldx; a.rows = out->rows; a.cols = out->cols;
+  a.codes = out->codes; a.ldq = out->ld; a.scale = out->scale;
+  a.vec = rows16(X, ldx, dtype_size(dt)) ? 1 : 0;
+  a.status = status;
+  const int64_t kb = cdiv(out->cols, kF8Block);
+  if (out->block_rows == 1) {
+    const int64_t grid = cdiv(out->rows * kb * 16, kF8QuantThreads);
+    if (grid > 0x7FFFFFFF) return QLORA_ERR_UNSUPPORTED;
+    if (dt == QLORA_BF16) k_fp8_quant_rows<__nv_bfloat16><<<static_cast<unsigned>(grid), kF8QuantThreads, 0, cs>>>(a);
+    else k_fp8_quant_rows<float><<<static_cast<unsigned>(grid), kF8QuantThreads, 0, cs>>>(a);
+  } else {
+    const int64_t grid = cdiv(out->rows, kF8Block) * kb;
+    if (grid > 0x7FFFFFFF) return QLORA_ERR_UNSUPPORTED;
+    if (dt == QLORA_BF16) k_fp8_quant_blocks<__nv_bfloat16><<<static_cast<unsigned>(grid), 256, 0, cs>>>(a);
+    else k_fp8_quant_blocks<float><<<static_cast<unsigned>(grid), 256, 0, cs>>>(a);
+  }
+  return check_launch();
+}
+
+// Token counts up to this take the weight-streaming kernel in the forward.
+constexpr int64_t kF8GemvMaxM = 32;
+
+qlora_status run_fp8_gemv(const qlora_fp8_matrix* Wq, const qlora_fp8_matrix* Xq, void* Y, qlora_dtype y_dtype,
+                          int64_t ldy, cudaStream_t cs) {
+  Fp8GemvArgs a{};
+  a.w = Wq->codes; a.ldw = Wq->ld; a.N = Wq->rows; a.K = Wq->cols; a.sw = Wq->scale;
+  a.x = Xq->codes; a.ldx = Xq->ld; a.M = static_cast<int>(Xq->rows); a.sx = Xq->scale;
+  a.y = Y; a.ldy = ldy; a.y_f32 = y_dtype == QLORA_F32 ? 1 : 0;
+  const unsigned grid = static_cast<unsigned>(cdiv(a.N, kF8GemvRows));
+  if (a.M <= 8) k_fp8_gemv<1><<<grid, kF8GemvWarps * 32, 0, cs>>>(a);
+  else if (a.M <= 16) k_fp8_gemv<2><<<grid, kF8GemvWarps * 32, 0, cs>>>(a);
+  else k_fp8_gemv<4><<<grid, kF8GemvWarps * 32, 0, cs>>>(a);
+  return check_launch();
+}
+
+qlora_status run_fp8_gemm(int mode, const qlora_fp8_matrix* Wq, const qlora_fp8_matrix* Aq, void* out,
+                          qlora_dtype o_dtype, int64_t ldo, int* status, cudaStream_t cs) {
+  const int64_t M = Aq->rows, out_cols = mode == 0 ? Wq->rows : Wq->cols;
+  const int64_t tm = cdiv(M, 256), tn = cdiv(out_cols, 256);
+  if (tm * tn > (int64_t(1) << 28)) return QLORA_ERR_UNSUPPORTED;
+  if (!ensure_smem_attrs()) return QLORA_ERR_CUDA;
+  const int sms = sm_count();
+  if (sms < 2) return QLORA_ERR_CUDA;
+  CUtensorMap ta, tw;
+  if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, Aq->codes, Aq->cols, M, Aq->ld, 128, 128,
+                CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq->codes, Wq->cols, Wq->rows, Wq->ld, 128, 128,
+                CU_TENSOR_MAP_SWIZZLE_128B))
+    return QLORA_ERR_CUDA;
+  Fp8GemmArgs a{};
+  a.M = M; a.out_cols = out_cols; a.ctr = mode == 0 ? Wq->cols : Wq->rows;
+  a.sa = Aq->scale; a.sw = Wq->scale; a.sw_cols = cdiv(Wq->cols, kF8Block);
+  a.out = out; a.ldo = ldo; a.out_f32 = o_dtype == QLORA_F32 ? 1 : 0;
+  a.out_vec = rows16(out, ldo, dtype_size(o_dtype)) ? 1 : 0;
+  a.tiles_m = static_cast<int>(tm); a.tiles_n = static_cast<int>(tn);
+  a.status = status;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(sms / 2, tm * tn)));
+  cfg.blockDim = dim3(kF8Threads);
+  cfg.dynamicSmemBytes = kF8SmemBytes;
+  cfg.stream = cs;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = mode == 0 ? cudaLaunchKernelEx(&cfg, k_fp8_gemm<0>, ta, tw, a)
+                                  : cudaLaunchKernelEx(&cfg, k_fp8_gemm<1>, ta, tw, a);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return QLORA_ERR_CUDA;
+  }
+  return QLORA_OK;
+}
+
+// Shared by the two directions: `in_cols` columns come in, `out_cols` go out.
+qlora_status fp8_linear(int mode, const void* X, qlora_dtype x_dtype, int64_t ldx, const qlora_fp8_matrix* Wq,
+                        const qlora_fp8_matrix* Xq, void* Y, qlora_dtype y_dtype, int64_t ldy, int* status,
+                        cudaStream_t cs) {
+  qlora_status st = check_fp8(Wq, kF8Block);
+  if (st != QLORA_OK) return st;
+  st = check_fp8(Xq, 1);
+  if (st != QLORA_OK) return st;
+  if (Wq->rows < 1) return QLORA_ERR_INVALID_ARG;
+  const int64_t in_cols = mode == 0 ? Wq->cols : Wq->rows, out_cols = mode == 0 ? Wq->rows : Wq->cols;
+  if (Xq->cols != in_cols || !is_io_dtype(y_dtype) || ldy < out_cols) return QLORA_ERR_INVALID_ARG;
+  if (X && (!is_io_dtype(x_dtype) || ldx < in_cols || !aligned_to(X, dtype_size(x_dtype)))) return QLORA_ERR_INVALID_ARG;
+  if (Xq->rows == 0) return QLORA_OK;
+  if (!Y || !aligned_to(Y, dtype_size(y_dtype))) return QLORA_ERR_INVALID_ARG;
+  if (X) {
+    st = run_fp8_quantize(X, x_dtype, ldx, Xq, status, cs);
+    if (st != QLORA_OK) return st;
+  }
+  if (mode == 0 && Xq->rows <= kF8GemvMaxM) return run_fp8_gemv(Wq, Xq, Y, y_dtype, ldy, cs);
+  return run_fp8_gemm(mode, Wq, Xq, Y, y_dtype, ldy, status, cs);
+}
+
+}  // namespace
+
+extern "C" {
+
+qlora_status qlora_fp8_sizes(int64_t rows, int64_t cols, int block_rows, size_t* codes_bytes, size_t* scale_bytes) {
+  if (rows < 0 || cols < 1 || (block_rows != 1 && block_rows != kF8Block) || !codes_bytes || !scale_bytes)
+    return QLORA_ERR_INVALID_ARG;
+  if (rows > (int64_t(1) << 30) || cols > (int64_t(1) << 30)) return QLORA_ERR_UNSUPPORTED;
+  *codes_bytes = static_cast<size_t>(rows) * rup(cols, kF8Block);
+  *scale_bytes = static_cast<size_t>(cdiv(rows, block_rows)) * cdiv(cols, kF8Block) * 4;
+  return QLORA_OK;
+}
+
+qlora_status qlora_fp8_quantize(const void* X, qlora_dtype x_dtype, int64_t ldx, const qlora_fp8_matrix* out,
+                                int* d_status, void* stream) {
+  NvtxRange nvtx_range("qlora_fp8_quantize");
+  const qlora_status st = check_fp8(out, 0);
+  if (st != QLORA_OK) return st;
+  if (!is_io_dtype(x_dtype) || ldx < out->cols) return QLORA_ERR_INVALID_ARG;
+  if (out->rows == 0) return QLORA_OK;
+  if (!X || !aligned_to(X, dtype_size(x_dtype))) return QLORA_ERR_INVALID_ARG;
+  return run_fp8_quantize(X, x_dtype, ldx, out, d_status, static_cast<cudaStream_t>(stream));
+}
+
+qlora_status qlora_fp8_linear_fwd(const void* X, qlora_dtype x_dtype, int64_t ldx, const qlora_fp8_matrix* Wq,
+                                  const qlora_fp8_matrix* Xq, void* Y, qlora_dtype y_dtype, int64_t ldy, int* d_status,
+                                  void* stream) {
+  NvtxRange nvtx_range("qlora_fp8_linear_fwd");
+  return fp8_linear(0, X, x_dtype, ldx, Wq, Xq, Y, y_dtype, ldy, d_status, static_cast<cudaStream_t>(stream));
+}
+
+qlora_status qlora_fp8_linear_bwd(const void* dY, qlora_dtype dy_dtype, int64_t lddy, const qlora_fp8_matrix* Wq,
+                                  const qlora_fp8_matrix* dYq, void* dX, qlora_dtype dx_dtype, int64_t lddx,
+                                  int* d_status, void* stream) {
+  NvtxRange nvtx_range("qlora_fp8_linear_bwd");
+  return fp8_linear(1, dY, dy_dtype, lddy, Wq, dYq, dX, dx_dtype, lddx, d_status, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ================================================================= layer norm
+namespace {
+
+// How a row is spread over threads: GROUP threads, PER chunks each; the
+// streaming kernels (group 0) take what fits no other.
+struct LnPlan {
+  int group, per;
+  bool vec;
+};
+LnPlan ln_plan(int64_t cols, int vec_elems, bool vec) {
+  if (vec) {
+    const int64_t n = cols / vec_elems;
+    if (n <= 32) return {32, 1, true};
+    if (n <= 64) return {32, 2, true};
+    if (n <= 128) return {32, 4, true};
+    if (n <= 256) return {128, 2, true};
+    if (n <= 512) return {256, 2, true};
+    if (n <= 1024) return {512, 2, true};
+    if (n <= 2048) return {1024, 2, true};
+    return {0, 0, false};
+  }
+  if (cols <= 128) return {32, 4, false};
+  if (cols <= 1024) return {128, 8, false};
+  if (cols <= 4096) return {512, 8, false};
+  if (cols <= 8192) return {1024, 8, false};
+  return {0, 0, false};
+}
+
+template <typename T, int VEC, int GROUP, int PER, bool BWD>
+int ln_launch(const LnArgs& a, int max_parts, cudaStream_t cs) {
+  constexpr int kRows = ln_block<GROUP>() / GROUP;
+  int64_t grid = cdiv(a.rows, kRows);
+  if (!BWD) {
+    k_ln_fwd<T, VEC, GROUP, PER><<<static_cast<unsigned>(grid), ln_block<GROUP>(), 0, cs>>>(a);
+    return 0;
+  }
+  // one wave of resident blocks
+  const int per_sm = std::max(1, 1024 / ln_block<GROUP>() / 2);
+  grid = std::min<int64_t>(grid, std::min<int64_t>(static_cast<int64_t>(sm_count()) * per_sm, max_parts / kRows));
+  k_ln_bwd<T, VEC, GROUP, PER><<<static_cast<unsigned>(grid), ln_block<GROUP>(), 0, cs>>>(a);
+  return static_cast<int>(grid * kRows);
+}
+
+// Launches the row kernel of a plan; returns the partial rows written.
+template <typename T, bool BWD>
+int ln_rows(const LnArgs& a, const LnPlan& p, int max_parts, cudaStream_t cs) {
+  constexpr int V = LnElem<T>::kVec;
+  if (p.vec) {
+    if (p.group == 32 && p.per == 1) return ln_launch<T, V, 32, 1, BWD>(a, max_parts, cs);
+    if (p.group == 32 && p.per == 2) return ln_launch<T, V, 32, 2, BWD>(a, max_parts, cs);
+    if (p.group == 32) return ln_launch<T, V, 32, 4, BWD>(a, max_parts, cs);
+    if (p.group == 128) return ln_launch<T, V, 128, 2, BWD>(a, max_parts, cs);
+    if (p.group == 256) return ln_launch<T, V, 256, 2, BWD>(a, max_parts, cs);
+    if (p.group == 512) return ln_launch<T, V, 512, 2, BWD>(a, max_parts, cs);
+    return ln_launch<T, V, 1024, 2, BWD>(a, max_parts, cs);
+  }
+  if (p.group == 32) return ln_launch<T, 1, 32, 4, BWD>(a, max_parts, cs);
+  if (p.group == 128) return ln_launch<T, 1, 128, 8, BWD>(a, max_parts, cs);
+  if (p.group == 512) return ln_launch<T, 1, 512, 8, BWD>(a, max_parts, cs);
+  return ln_launch<T, 1, 1024, 8, BWD>(a, max_parts, cs);
+}
+
+// Run any row length backward: partials first (dX may overwrite an input), then dX.
+template <typename T>
+int ln_bwd_stream(const LnArgs& a, int max_parts, cudaStream_t cs) {
+  int parts = 0;
+  if (a.part) {
+    const int64_t col_blocks = cdiv(a.cols, kLnColThreads);
+    const int64_t want = std::max<int64_t>(1, 8LL * sm_count() / col_blocks);
+    parts = static_cast<int>(std::min<int64_t>(std::min<int64_t>(want, max_parts), a.rows));
+    k_ln_bwd_cols<T><<<dim3(static_cast<unsigned>(col_blocks), static_cast<unsigned>(parts)), kLnColThreads, 0, cs>>>(a);
+  }
+  k_ln_bwd_stream<T><<<static_cast<unsigned>(a.rows), kLnStreamThreads, 0, cs>>>(a);
+  return parts;
+}
+
+bool ln_shape(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 1 && rows < (int64_t(1) << 31) && cols < (int64_t(1) << 31);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qlora_layernorm_workspace_bytes(int64_t rows, int64_t cols) {
+  if (!ln_shape(rows, cols)) return 0;
+  // a group of a warp has company in its block: whole blocks write partials
+  return static_cast<size_t>(std::min<int64_t>(rup(rows, 4), kLnMaxParts)) * 2 * cols * 4;
+}
+
+qlora_status qlora_layernorm_fwd(const void* X, int64_t ldx, int64_t rows, int64_t cols, qlora_dtype dtype,
+                                 const void* weight, const void* bias, qlora_dtype w_dtype, float eps, void* Y,
+                                 int64_t ldy, float* mean, float* rstd, void* stream) {
+  NvtxRange nvtx_range("qlora_layernorm_fwd");
+  if (!ln_shape(rows, cols) || ldx < cols || ldy < cols || !is_io_dtype(dtype) || !is_io_dtype(w_dtype))
+    return QLORA_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.0f) return QLORA_ERR_INVALID_ARG;
+  if (rows == 0) return QLORA_OK;
+  const size_t es = dtype_size(dtype), wsz = dtype_size(w_dtype);
+  if (!X || !Y || !aligned_to(X, es) || !aligned_to(Y, es) || !aligned_to(weight, wsz) || !aligned_to(bias, wsz) ||
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return QLORA_ERR_INVALID_ARG;
+  LnArgs a{};
+  a.x = X; a.ldx = ldx; a.w = weight; a.b = bias; a.w_bf16 = w_dtype == QLORA_BF16 ? 1 : 0;
+  a.rows = rows; a.cols = cols; a.eps = eps; a.y = Y; a.ldy = ldy; a.mean = mean; a.rstd = rstd;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const int v = dtype == QLORA_BF16 ? LnElem<__nv_bfloat16>::kVec : LnElem<float>::kVec;
+  const bool vec = cols % v == 0 && rows16(X, ldx, es) && rows16(Y, ldy, es) && aligned16(weight) && aligned16(bias);
+  const LnPlan p = ln_plan(cols, v, vec);
+  if (p.group == 0) {
+    if (dtype == QLORA_BF16) k_ln_fwd_stream<__nv_bfloat16><<<static_cast<unsigned>(rows), kLnStreamThreads, 0, cs>>>(a);
+    else k_ln_fwd_stream<float><<<static_cast<unsigned>(rows), kLnStreamThreads, 0, cs>>>(a);
+  } else if (dtype == QLORA_BF16) {
+    ln_rows<__nv_bfloat16, false>(a, p, 0, cs);
+  } else {
+    ln_rows<float, false>(a, p, 0, cs);
+  }
+  return check_launch();
+}
+
+qlora_status qlora_layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx, int64_t rows, int64_t cols,
+                                 qlora_dtype dtype, const void* weight, qlora_dtype w_dtype, const float* mean,
+                                 const float* rstd, void* dX, int64_t lddx, void* dweight, void* dbias,
+                                 qlora_dtype grad_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("qlora_layernorm_bwd");
+  if (!ln_shape(rows, cols) || ldx < cols || lddy < cols || lddx < cols || !is_io_dtype(dtype) ||
+      !is_io_dtype(w_dtype) || !is_io_dtype(grad_dtype))
+    return QLORA_ERR_INVALID_ARG;
+  const size_t es = dtype_size(dtype), gs = dtype_size(grad_dtype);
+  if (!aligned_to(weight, dtype_size(w_dtype)) || !aligned_to(dweight, gs) || !aligned_to(dbias, gs))
+    return QLORA_ERR_INVALID_ARG;
+  if (rows > 0 && (!dY || !X || !dX || !mean || !rstd || !aligned_to(dY, es) || !aligned_to(X, es) ||
+                   !aligned_to(dX, es) || !aligned_to(mean, 4) || !aligned_to(rstd, 4)))
+    return QLORA_ERR_INVALID_ARG;
+  const bool want = dweight || dbias;
+  if (want && rows > 0) {
+    if (!workspace || !aligned16(workspace) || ws_bytes < qlora_layernorm_workspace_bytes(rows, cols))
+      return QLORA_ERR_WORKSPACE;
+  }
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  int parts = 0;
+  if (rows > 0) {
+    if (sm_count() <= 0) return QLORA_ERR_CUDA;
+    LnArgs a{};
+    a.x = X; a.ldx = ldx; a.w = weight; a.w_bf16 = w_dtype == QLORA_BF16 ? 1 : 0;
+    a.rows = rows; a.cols = cols; a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
+    a.dy = dY; a.lddy = lddy; a.dx = dX; a.lddx = lddx;
+    a.part = want ? static_cast<float*>(workspace) : nullptr;
+    const int v = dtype == QLORA_BF16 ? LnElem<__nv_bfloat16>::kVec : LnElem<float>::kVec;
+    const bool vec = cols % v == 0 && rows16(X, ldx, es) && rows16(dY, lddy, es) && rows16(dX, lddx, es) &&
+                     aligned16(weight);
+    const LnPlan p = ln_plan(cols, v, vec);
+    const int max_parts = static_cast<int>(std::min<int64_t>(rup(rows, 4), kLnMaxParts));
+    if (p.group == 0)
+      parts = dtype == QLORA_BF16 ? ln_bwd_stream<__nv_bfloat16>(a, max_parts, cs) : ln_bwd_stream<float>(a, max_parts, cs);
+    else
+      parts = dtype == QLORA_BF16 ? ln_rows<__nv_bfloat16, true>(a, p, max_parts, cs)
+                                  : ln_rows<float, true>(a, p, max_parts, cs);
+    const qlora_status st = check_launch();
+    if (st != QLORA_OK) return st;
+  }
+  if (want) {
+    LnFinishArgs f{};
+    f.part = static_cast<const float*>(workspace);
+    f.parts = parts; f.cols = cols; f.dw = dweight; f.db = dbias; f.out_bf16 = grad_dtype == QLORA_BF16 ? 1 : 0;
+    k_ln_finish<<<static_cast<unsigned>(cdiv(cols, 32)), 1024, 0, cs>>>(f);
+    return check_launch();
+  }
+  return QLORA_OK;
+}
+
+}  // extern "C"
+
+// ================================================================ distillation
+namespace {
+
+qlora_status check_distill(const void* Z, int64_t ldz, int64_t rows, int64_t vocab, qlora_dtype dtype, const void* ids,
+                           int id_bits, const void* t, qlora_dtype t_dtype, int top, float tau, const float* row_weight,
+                           const void* dZ, int64_t lddz) {
+  if (rows < 0 || vocab < 1 || ldz < vocab || !is_io_dtype(dtype) || !is_io_dtype(t_dtype)) return QLORA_ERR_INVALID_ARG;
+  if ((id_bits != 32 && id_bits != 64) || top < 1 || top > kDiMaxTop) return QLORA_ERR_INVALID_ARG;
+  if (!std::isfinite(tau) || !(tau > 0.0f) || !std::isfinite(1.0f / tau) || !std::isfinite(tau * tau))
+    return QLORA_ERR_INVALID_ARG;
+  if (dZ && lddz < vocab) return QLORA_ERR_INVALID_ARG;
+  if (vocab >= (int64_t(1) << 31) || rows > (int64_t(1) << 27)) return QLORA_ERR_UNSUPPORTED;
+  if (rows == 0) return QLORA_OK;
+  const size_t es = dtype_size(dtype);
+  if (!Z || !ids || !t || !aligned_to(Z, es) || !aligned_to(ids, id_bits / 8) || !aligned_to(t, dtype_size(t_dtype)) ||
+      !aligned_to(row_weight, 4) || !aligned_to(dZ, es))
+    return QLORA_ERR_INVALID_ARG;
+  if (dZ == Z && dZ && lddz != ldz) return QLORA_ERR_INVALID_ARG;
+  return QLORA_OK;
+}
+
+// CTAs per row: enough to give every SM two CTAs, as long as a slice keeps
+// a few thousand logits (below that a CTA is mostly its fixed cost).
+int distill_slices(int64_t rows, int64_t vocab) {
+  const int64_t ctas = 2LL * std::max(1, sm_count());
+  int s = 1;
+  while (s < 8 && rows * s < ctas && vocab / (2 * s) >= 4096) s *= 2;
+  return s;
+}
+
+template <bool FWD>
+qlora_status run_distill(DistillArgs& a, qlora_dtype dtype, cudaStream_t cs) {
+  a.slices = distill_slices(a.rows, a.vocab);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows * a.slices));
+  cfg.blockDim = dim3(kDiThreads);
+  cfg.stream = cs;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(FWD ? a.slices : 1);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = dtype == QLORA_BF16 ? cudaLaunchKernelEx(&cfg, k_distill<__nv_bfloat16, FWD>, a)
+                                            : cudaLaunchKernelEx(&cfg, k_distill<float, FWD>, a);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return QLORA_ERR_CUDA;
+  }
+  return QLORA_OK;
+}
+
+DistillArgs distill_args(const void* Z, int64_t ldz, int64_t rows, int64_t vocab, const void* ids, int id_bits,
+                         const void* t, qlora_dtype t_dtype, int top, float tau, const float* row_weight, void* dZ,
+                         int64_t lddz, int* status) {
+  DistillArgs a{};
+  a.z = Z; a.ldz = ldz; a.rows = rows; a.vocab = vocab;
+  a.ids = ids; a.ids64 = id_bits == 64 ? 1 : 0;
+  a.t = t; a.t_bf16 = t_dtype == QLORA_BF16 ? 1 : 0; a.top = top;
+  a.weight = row_weight; a.tau = tau;
+  a.scale2 = static_cast<float>(1.4426950408889634 / static_cast<double>(tau));
+  a.dz = dZ; a.lddz = lddz; a.status = status;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+qlora_status qlora_distill_topk_fwd(const void* Z, int64_t ldz, int64_t rows, int64_t vocab, qlora_dtype dtype,
+                                    const void* ids, int id_bits, const void* t, qlora_dtype t_dtype, int top,
+                                    float tau, const float* row_weight, float* loss, float* lse, void* dZ,
+                                    int64_t lddz, int* d_status, void* stream) {
+  NvtxRange nvtx_range("qlora_distill_topk_fwd");
+  const qlora_status st =
+      check_distill(Z, ldz, rows, vocab, dtype, ids, id_bits, t, t_dtype, top, tau, row_weight, dZ, lddz);
+  if (st != QLORA_OK) return st;
+  if (rows == 0) return QLORA_OK;
+  if (!loss || !aligned_to(loss, 4) || !aligned_to(lse, 4)) return QLORA_ERR_INVALID_ARG;
+  DistillArgs a = distill_args(Z, ldz, rows, vocab, ids, id_bits, t, t_dtype, top, tau, row_weight, dZ, lddz, d_status);
+  a.loss = loss;
+  a.lse = lse;
+  return run_distill<true>(a, dtype, static_cast<cudaStream_t>(stream));
+}
+
+qlora_status qlora_distill_topk_bwd(const void* Z, int64_t ldz, int64_t rows, int64_t vocab, qlora_dtype dtype,
+                                    const void* ids, int id_bits, const void* t, qlora_dtype t_dtype, int top,
+                                    float tau, const float* row_weight, const float* lse, const float* grad_loss,
+                                    void* dZ, int64_t lddz, int* d_status, void* stream) {
+  NvtxRange nvtx_range("qlora_distill_topk_bwd");
+  const qlora_status st =
+      check_distill(Z, ldz, rows, vocab, dtype, ids, id_bits, t, t_dtype, top, tau, row_weight, dZ, lddz);
+  if (st != QLORA_OK) return st;
+  if (rows == 0) return QLORA_OK;
+  if (!dZ || !lse || !aligned_to(lse, 4) || !aligned_to(grad_loss, 4)) return QLORA_ERR_INVALID_ARG;
+  DistillArgs a = distill_args(Z, ldz, rows, vocab, ids, id_bits, t, t_dtype, top, tau, row_weight, dZ, lddz, d_status);
+  a.lse_in = lse;
+  a.grad = grad_loss;
+  return run_distill<false>(a, dtype, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

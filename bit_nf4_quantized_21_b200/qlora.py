@@ -8,6 +8,7 @@ tensor is not on a CUDA device, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -25,6 +26,7 @@ QLORA_F32 = 0
 QLORA_BF16 = 1
 DEV_NONFINITE = 1
 DEV_TIMEOUT = 2
+DEV_INDEX = 4
 
 EXPORTED = (
     "qlora_nf4_sizes", "qlora_nf4_codebook", "qlora_quantize_nf4", "qlora_dequantize",
@@ -34,7 +36,9 @@ EXPORTED = (
     "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout", "qlora_paged_alloc", "qlora_paged_free",
     "qlora_paged_prefetch", "qlora_debug_set_wait_limit", "qlora_debug_inject_stall",
     "qlora_debug_set_pair_mtiles", "qlora_debug_checks_enabled", "qlora_debug_range_check",
-    "qlora_debug_range_selftest",
+    "qlora_debug_range_selftest", "qlora_fp8_sizes", "qlora_fp8_quantize", "qlora_fp8_linear_fwd",
+    "qlora_fp8_linear_bwd", "qlora_layernorm_workspace_bytes", "qlora_layernorm_fwd", "qlora_layernorm_bwd",
+    "qlora_distill_topk_fwd", "qlora_distill_topk_bwd",
 )
 
 
@@ -65,6 +69,14 @@ class NF4WeightC(ctypes.Structure):
         ("double_quant", ctypes.c_int32), ("reserved", ctypes.c_int32),
         ("codes", ctypes.c_void_p), ("absmax_q8", ctypes.c_void_p),
         ("group_scale", ctypes.c_void_p), ("absmax_f32", ctypes.c_void_p),
+    ]
+
+
+class FP8MatrixC(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64),
+        ("block_rows", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
     ]
 
 
@@ -142,6 +154,25 @@ def lib() -> ctypes.CDLL:
             L.qlora_debug_range_check.restype = I32
             L.qlora_debug_range_selftest.argtypes = [P]
             L.qlora_debug_range_selftest.restype = I32
+            FP8 = ctypes.POINTER(FP8MatrixC)
+            L.qlora_fp8_sizes.argtypes = [I64, I64, I32, P, P]
+            L.qlora_fp8_sizes.restype = I32
+            L.qlora_fp8_quantize.argtypes = [P, I32, I64, FP8, P, P]
+            L.qlora_fp8_quantize.restype = I32
+            for f in (L.qlora_fp8_linear_fwd, L.qlora_fp8_linear_bwd):
+                f.argtypes = [P, I32, I64, FP8, FP8, P, I32, I64, P, P]
+                f.restype = I32
+            L.qlora_layernorm_workspace_bytes.argtypes = [I64, I64]
+            L.qlora_layernorm_workspace_bytes.restype = ctypes.c_size_t
+            L.qlora_layernorm_fwd.argtypes = [P, I64, I64, I64, I32, P, P, I32, F, P, I64, P, P, P]
+            L.qlora_layernorm_fwd.restype = I32
+            L.qlora_layernorm_bwd.argtypes = [P, I64, P, I64, I64, I64, I32, P, I32, P, P, P, I64, P, P, I32, P,
+                                              ctypes.c_size_t, P]
+            L.qlora_layernorm_bwd.restype = I32
+            L.qlora_distill_topk_fwd.argtypes = [P, I64, I64, I64, I32, P, I32, P, I32, I32, F, P, P, P, P, I64, P, P]
+            L.qlora_distill_topk_fwd.restype = I32
+            L.qlora_distill_topk_bwd.argtypes = [P, I64, I64, I64, I32, P, I32, P, I32, I32, F, P, P, P, P, I64, P, P]
+            L.qlora_distill_topk_bwd.restype = I32
             L.qlora_status_string.argtypes = [I32]
             L.qlora_status_string.restype = ctypes.c_char_p
             L.qlora_version.argtypes = []
@@ -489,3 +520,282 @@ def qlora_paged_prefetch(ptr: int, nbytes: int, to_device: bool = True, stream=N
     """Migrate [ptr, ptr + nbytes) to the current GPU, or page it out to the host."""
     _check(lib().qlora_paged_prefetch(ptr, int(nbytes), 1 if to_device else 0, _stream(stream)),
            "qlora_paged_prefetch")
+
+
+# --------------------------------------- strided operands of the calls below
+
+_DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name} must be fp32 or bf16")
+    return d
+
+
+def _matrix(t: torch.Tensor, name: str, rows: int | None = None, cols: int | None = None) -> tuple[int, int]:
+    """(pointer, elements between rows) of a 2-D tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("libqlora takes CUDA tensors only")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be 2-D [{'rows' if rows is None else rows}, {'cols' if cols is None else cols}]"
+                         f", got {tuple(t.shape)}")
+    n, c = t.shape
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    ld = t.stride(0) if n > 1 else c
+    if ld < c:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), ld
+
+
+def _vector(t: torch.Tensor | None, name: str, n: int, dtype=None) -> int | None:
+    if t is None:
+        return None
+    if t.numel() != n or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must have {n} elements" + (f" of {dtype}" if dtype is not None else ""))
+    return _ptr(t)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream, *tensors):
+    """The context of a call: its tensors' one device made current, and its
+    stream, so that what the call allocates belongs to the stream that uses it."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors of a call must be on one CUDA device")
+    if dev.type != "cuda":
+        raise ValueError("libqlora takes CUDA tensors only")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("the stream must belong to the tensors' device")
+        return torch.cuda.stream(stream)
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+# ------------------------------------------------------------- FP8 linear layer
+
+@dataclass
+class FP8Matrix:
+    """A matrix as E4M3 codes with one fp32 scale for each block of 128 (see qlora_fp8_matrix)."""
+    rows: int
+    cols: int
+    block_rows: int                     # 128: weights, 1: activations
+    codes: torch.Tensor                 # uint8 (or float8_e4m3fn) [rows, ld]
+    scale: torch.Tensor                 # fp32 [ceil(rows/128), ceil(cols/128)], or [ceil(cols/128), rows]
+
+    def c(self) -> FP8MatrixC:
+        if self.codes.element_size() != 1 or self.scale.dtype != torch.float32:
+            raise ValueError("codes are bytes and scales fp32")
+        p, ld = _matrix(self.codes, "codes", self.rows)
+        if self.codes.shape[1] < -(-self.cols // 16) * 16:
+            raise ValueError("codes: a row holds cols rounded up to 16 bytes")
+        want = -(-self.rows // self.block_rows) * -(-self.cols // 128) if self.block_rows in (1, 128) else -1
+        return FP8MatrixC(self.rows, self.cols, ld, self.block_rows, 0, p, _vector(self.scale, "scale", want))
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scale.numel()
+
+
+def qlora_fp8_sizes(rows: int, cols: int, block_rows: int = 128) -> tuple[int, int]:
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().qlora_fp8_sizes(rows, cols, block_rows, ctypes.byref(c), ctypes.byref(s)), "qlora_fp8_sizes")
+    return c.value, s.value
+
+
+def empty_fp8(rows: int, cols: int, device, block_rows: int = 128) -> FP8Matrix:
+    """Allocate (torch) the arrays of an FP8 matrix."""
+    kb = -(-cols // 128)
+    codes = torch.empty((rows, kb * 128), dtype=torch.uint8, device=device)
+    shape = (kb, rows) if block_rows == 1 else (-(-rows // 128), kb)
+    return FP8Matrix(rows, cols, block_rows, codes, torch.empty(shape, dtype=torch.float32, device=device))
+
+
+def qlora_fp8_quantize(X: torch.Tensor, out: FP8Matrix | None = None, block_rows: int = 128,
+                       d_status: torch.Tensor | None = None, stream=None) -> FP8Matrix:
+    """E4M3 codes and scales of X: block_rows = 128 for a weight, 1 for activations."""
+    dt = _dtype(X, "X")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows is 1 or 128")
+    with _on(stream, X, d_status, *(() if out is None else (out.codes, out.scale))):
+        if out is None:
+            out = empty_fp8(X.shape[0], X.shape[1], X.device, block_rows)
+        p, ld = _matrix(X, "X", out.rows, out.cols)
+        _check(lib().qlora_fp8_quantize(p, dt, ld, ctypes.byref(out.c()), _ptr(d_status), _stream()),
+               "qlora_fp8_quantize")
+    return out
+
+
+def _fp8_linear(where, X, Wq, out, out_dtype, Xq, d_status, stream, in_cols, out_cols):
+    with _on(stream, Wq.codes, Wq.scale, out, d_status,
+             *((X.codes, X.scale) if isinstance(X, FP8Matrix) else (X,)),
+             *(() if Xq is None else (Xq.codes, Xq.scale))):
+        if isinstance(X, FP8Matrix):
+            if Xq is not None:
+                raise ValueError("already quantised activations need no scratch")
+            p, dt, ld, Xq = None, QLORA_F32, 0, X
+        else:
+            p, ld = _matrix(X, "activations", cols=in_cols)
+            dt = _dtype(X, "activations")
+            if Xq is None:
+                Xq = empty_fp8(X.shape[0], in_cols, X.device, 1)
+            elif Xq.rows != X.shape[0]:
+                raise ValueError("the scratch must have the activations' rows")
+        if out is None:
+            out = torch.empty((Xq.rows, out_cols), dtype=out_dtype, device=Wq.codes.device)
+        o, ldo = _matrix(out, "output", Xq.rows, out_cols)
+        _check(getattr(lib(), where)(p, dt, ld, ctypes.byref(Wq.c()), ctypes.byref(Xq.c()), o, _dtype(out, "output"),
+                                     ldo, _ptr(d_status), _stream()), where)
+    return out
+
+
+def qlora_fp8_linear_fwd(X: torch.Tensor | FP8Matrix, Wq: FP8Matrix, Y: torch.Tensor | None = None,
+                         out_dtype=torch.bfloat16, Xq: FP8Matrix | None = None,
+                         d_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = Q(X) W^T.  X: fp32 or bf16 [M, K], or an FP8Matrix (block_rows = 1) of them; Xq: where the
+    quantised X goes (allocated when not given)."""
+    return _fp8_linear("qlora_fp8_linear_fwd", X, Wq, Y, out_dtype, Xq, d_status, stream, Wq.cols, Wq.rows)
+
+
+def qlora_fp8_linear_bwd(dY: torch.Tensor | FP8Matrix, Wq: FP8Matrix, dX: torch.Tensor | None = None,
+                         out_dtype=torch.bfloat16, dYq: FP8Matrix | None = None,
+                         d_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dX = Q(dY) W for dY [M, N]; the frozen weight has no gradient."""
+    return _fp8_linear("qlora_fp8_linear_bwd", dY, Wq, dX, out_dtype, dYq, d_status, stream, Wq.rows, Wq.cols)
+
+
+# ------------------------------------------------------------------- layer norm
+
+def qlora_layernorm_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().qlora_layernorm_workspace_bytes(rows, cols))
+
+
+def _params(cols: int, *ps):
+    """(pointers, dtype) of weight and bias, which share one type."""
+    given = [p for p in ps if p is not None]
+    if any(p.dtype != given[0].dtype for p in given):
+        raise ValueError("weight and bias must have one type")
+    return [_vector(p, "weight and bias", cols) for p in ps], _dtype(given[0], "weight and bias") if given else QLORA_F32
+
+
+def qlora_layernorm_fwd(X: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                        eps: float = 1e-5, Y: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                        rstd: torch.Tensor | None = None, stream=None):
+    """(Y, mean, rstd) of the rows of X [rows, cols]; mean and rstd (fp32 [rows]) are what the backward needs."""
+    with _on(stream, X, weight, bias, Y, mean, rstd):
+        x, ldx = _matrix(X, "X")
+        rows, cols = X.shape
+        (w, b), wdt = _params(cols, weight, bias)
+        if Y is None:
+            Y = torch.empty((rows, cols), dtype=X.dtype, device=X.device)
+        elif Y.dtype != X.dtype:
+            raise ValueError("Y has X's type")
+        y, ldy = _matrix(Y, "Y", rows, cols)
+        if mean is None:
+            mean = torch.empty(rows, dtype=torch.float32, device=X.device)
+        if rstd is None:
+            rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
+        _check(lib().qlora_layernorm_fwd(x, ldx, rows, cols, _dtype(X, "X"), w, b, wdt, float(eps), y, ldy,
+                                         _vector(mean, "mean", rows, torch.float32),
+                                         _vector(rstd, "rstd", rows, torch.float32), _stream()),
+               "qlora_layernorm_fwd")
+    return Y, mean, rstd
+
+
+def qlora_layernorm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
+                        rstd: torch.Tensor, dX: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
+                        dbias: torch.Tensor | None = None, grad_dtype=torch.float32, want_params: bool = True,
+                        workspace: torch.Tensor | None = None, stream=None):
+    """(dX, dweight, dbias); want_params=False for a frozen norm (the two are None, unless given)."""
+    with _on(stream, dY, X, weight, mean, rstd, dX, dweight, dbias, workspace):
+        x, ldx = _matrix(X, "X")
+        rows, cols = X.shape
+        dy, lddy = _matrix(dY, "dY", rows, cols)
+        (w,), wdt = _params(cols, weight)
+        if dX is None:
+            dX = torch.empty((rows, cols), dtype=X.dtype, device=X.device)
+        if dY.dtype != X.dtype or dX.dtype != X.dtype:
+            raise ValueError("dY and dX have X's type")
+        dx, lddx = _matrix(dX, "dX", rows, cols)
+        if want_params:
+            gt = dweight.dtype if dweight is not None else dbias.dtype if dbias is not None else grad_dtype
+            if dweight is None:
+                dweight = torch.empty(cols, dtype=gt, device=X.device)
+            if dbias is None:
+                dbias = torch.empty(cols, dtype=gt, device=X.device)
+        gdt = QLORA_F32
+        for g in (dweight, dbias):
+            if g is not None:
+                gdt = _dtype(g, "dweight and dbias")
+        if dweight is not None and dbias is not None and dweight.dtype != dbias.dtype:
+            raise ValueError("dweight and dbias must have one type")
+        ws, ws_bytes = None, 0
+        if dweight is not None or dbias is not None:
+            if workspace is None:
+                workspace = torch.empty(max(qlora_layernorm_workspace_bytes(rows, cols), 16), dtype=torch.uint8,
+                                        device=X.device)
+            ws, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+        _check(lib().qlora_layernorm_bwd(dy, lddy, x, ldx, rows, cols, _dtype(X, "X"), w, wdt,
+                                         _vector(mean, "mean", rows, torch.float32),
+                                         _vector(rstd, "rstd", rows, torch.float32), dx, lddx,
+                                         _vector(dweight, "dweight", cols), _vector(dbias, "dbias", cols), gdt, ws,
+                                         ws_bytes, _stream()), "qlora_layernorm_bwd")
+    return dX, dweight, dbias
+
+
+# ----------------------------------------------------------------- distillation
+
+def _distill(Z, ids, t, row_weight, dZ):
+    z, ldz = _matrix(Z, "Z")
+    rows, vocab = Z.shape
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids are int32 or int64")
+    if ids.dim() != 2 or ids.shape[0] != rows or t.shape != ids.shape:
+        raise ValueError("ids and t must be [rows, top]")
+    if dZ is not None and dZ.dtype != Z.dtype:
+        raise ValueError("dZ has Z's type")
+    d, lddz = (None, 0) if dZ is None else _matrix(dZ, "dZ", rows, vocab)
+    if dZ is not None and rows == 1 and d == z:
+        lddz = ldz
+    return ((z, ldz, rows, vocab, _dtype(Z, "Z"), _ptr(ids), 32 if ids.dtype == torch.int32 else 64, _ptr(t),
+             _dtype(t, "t"), ids.shape[1]), _vector(row_weight, "row_weight", rows, torch.float32), (d, lddz))
+
+
+def qlora_distill_topk_fwd(Z: torch.Tensor, ids: torch.Tensor, t: torch.Tensor, tau: float = 1.0,
+                           row_weight: torch.Tensor | None = None, loss: torch.Tensor | None = None,
+                           lse: torch.Tensor | None = None, dZ: torch.Tensor | None = None,
+                           d_status: torch.Tensor | None = None, stream=None):
+    """(loss, lse), fp32 [rows], of student logits Z [rows, vocab] against a teacher's top logits t at ids
+    [rows, top] (negative ids: unused places).  With dZ (Z itself, or a tensor like it) the same launch
+    writes the gradient of the sum of the losses."""
+    with _on(stream, Z, ids, t, row_weight, loss, lse, dZ, d_status):
+        args, w, d = _distill(Z, ids, t, row_weight, dZ)
+        rows = Z.shape[0]
+        if loss is None:
+            loss = torch.empty(rows, dtype=torch.float32, device=Z.device)
+        if lse is None:
+            lse = torch.empty(rows, dtype=torch.float32, device=Z.device)
+        _check(lib().qlora_distill_topk_fwd(*args, float(tau), w, _vector(loss, "loss", rows, torch.float32),
+                                            _vector(lse, "lse", rows, torch.float32), *d, _ptr(d_status), _stream()),
+               "qlora_distill_topk_fwd")
+    return loss, lse
+
+
+def qlora_distill_topk_bwd(Z: torch.Tensor, ids: torch.Tensor, t: torch.Tensor, tau: float, lse: torch.Tensor,
+                           row_weight: torch.Tensor | None = None, grad_loss: torch.Tensor | None = None,
+                           dZ: torch.Tensor | None = None, d_status: torch.Tensor | None = None,
+                           stream=None) -> torch.Tensor:
+    """The gradient of the losses (weighted by grad_loss) with respect to Z, from the forward's lse."""
+    with _on(stream, Z, ids, t, row_weight, lse, grad_loss, dZ, d_status):
+        if dZ is None:
+            dZ = torch.empty(Z.shape, dtype=Z.dtype, device=Z.device)
+        args, w, d = _distill(Z, ids, t, row_weight, dZ)
+        rows = Z.shape[0]
+        _check(lib().qlora_distill_topk_bwd(*args, float(tau), w, _vector(lse, "lse", rows, torch.float32),
+                                            _vector(grad_loss, "grad_loss", rows, torch.float32), *d, _ptr(d_status),
+                                            _stream()), "qlora_distill_topk_bwd")
+    return dZ

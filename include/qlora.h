@@ -20,14 +20,16 @@
  *     dX [M, K]; adapters A [r, K], B [N, r]; s = alpha / r.
  *   - Array arguments are DEVICE pointers owned by the caller, except where a
  *     comment says host.  bf16 arrays are passed as void*.  Every device
- *     pointer must be 16-byte aligned.
+ *     pointer must be 16-byte aligned, except where a call says otherwise.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  Arguments are validated synchronously; the work is enqueued
  *     asynchronously on `stream`.  No call allocates memory, synchronises, or
  *     keeps state between calls.
  *   - `d_status` (nullable) is a device int the kernels OR error bits into:
- *     QLORA_DEV_NONFINITE_BIT (a non-finite weight seen by the quantiser or
- *     the merge, or a non-finite gradient seen by the Adam step) and
+ *     QLORA_DEV_NONFINITE_BIT (a non-finite weight seen by a quantiser or
+ *     the merge, or a non-finite gradient seen by the Adam step),
+ *     QLORA_DEV_INDEX_BIT (a vocabulary index past the end, in the
+ *     distillation loss) and
  *     QLORA_DEV_TIMEOUT_BIT (a pipeline wait gave up after ~2 s, or the
  *     bound set by qlora_debug_set_wait_limit; the kernel then returns
  *     early and its outputs are unspecified).  The caller zeroes
@@ -60,6 +62,7 @@ typedef enum {
 
 #define QLORA_DEV_NONFINITE_BIT 1
 #define QLORA_DEV_TIMEOUT_BIT 2
+#define QLORA_DEV_INDEX_BIT 4
 
 typedef enum { QLORA_F32 = 0, QLORA_BF16 = 1 } qlora_dtype;
 
@@ -332,6 +335,146 @@ qlora_status qlora_adam_step(float* master, float* m, float* v, void* param_bf16
                              int64_t step, float lr, float beta1, float beta2, float eps,
                              float weight_decay, float grad_scale, int* d_status,
                              void* stream);
+
+/*
+ * The frozen linear layer over a weight in 8-bit floating point (E4M3), one
+ * fp32 scale for each block of 128: the 8-bit sibling of the NF4 layer, for
+ * projections and output heads kept at 8 bits ("QLoRA", scalata.ai, the
+ * paragraph on checkpoints that come compressed to FP8).  No adapter.
+ *
+ * One matrix in this format.  Caller-owned device arrays.
+ *   block_rows  128 (weights: a scale for each 128 x 128 block) or 1
+ *               (activations: a scale for each 1 x 128 block); the last
+ *               blocks of a row or column may be short.
+ *   codes       [rows, ld] E4M3 bytes; ld >= cols, a multiple of 16; what
+ *               bytes cols .. ld - 1 of a row hold never matters.
+ *   scale       fp32; block_rows = 128: [ceil(rows/128), ceil(cols/128)];
+ *               block_rows = 1: [ceil(cols/128), rows] (block-major).  The
+ *               value of an element is E4M3(code) * scale of its block.
+ */
+typedef struct {
+  int64_t rows;
+  int64_t cols;
+  int64_t ld;
+  int32_t block_rows;   /* 1 or 128 */
+  int32_t reserved;     /* must be 0 */
+  uint8_t* codes;       /* 16-byte aligned */
+  float* scale;         /* 4-byte aligned */
+} qlora_fp8_matrix;
+
+/*
+ * Byte sizes of the arrays above for ld = cols rounded up to 128.  Host-only.
+ */
+qlora_status qlora_fp8_sizes(int64_t rows, int64_t cols, int block_rows, size_t* codes_bytes,
+                             size_t* scale_bytes);
+
+/*
+ * Quantise X [rows, cols] (fp32 or bf16, rows ldx elements apart, ldx >=
+ * cols, aligned to its element) into `out`: per block s = fp32(absmax / 448),
+ * code = E4M3(fp32(x * fp32(1/s))), round to nearest even, saturating.  A
+ * block whose s is below the smallest normal fp32 is stored as zeros with
+ * s = 0.  A non-finite element sets QLORA_DEV_NONFINITE_BIT and makes every
+ * output that depends on it NaN or, through a block maximum of infinity, NaN
+ * or zero.  rows = 0 is a no-op.
+ */
+qlora_status qlora_fp8_quantize(const void* X, qlora_dtype x_dtype, int64_t ldx,
+                                const qlora_fp8_matrix* out, int* d_status, void* stream);
+
+/*
+ * Forward and backward of the layer, Wq [N, K] with block_rows = 128:
+ *     forward   Y  = Q(X)  W^T   [M, N]     X  [M, K] quantised along K
+ *     backward  dX = Q(dY) W     [M, K]     dY [M, N] quantised along N
+ * Q is the 1 x 128 quantiser above.  Two forms of the activations:
+ *   X (dY) non-NULL: fp32 or bf16 (x_dtype), ldx elements between rows; it
+ *     is quantised into *Xq, which must be [M, K] ([M, N]) with block_rows =
+ *     1 and serves as the call's scratch (it can be used again afterwards);
+ *   X (dY) NULL: *Xq already holds the quantised activations, so that
+ *     several layers that read one input quantise it once.
+ * The rows of *Xq are M.  Y (dX): y_dtype fp32 or bf16, ldy elements between
+ * rows, aligned to its element; columns past the last are left alone.  Each
+ * block's products are summed exactly enough for fp32 and the scaled sums
+ * added in fp32; the output is rounded once.  Any N, K >= 1; M = 0 is a
+ * no-op.  Deterministic.  The outputs may not overlap the inputs.
+ */
+qlora_status qlora_fp8_linear_fwd(const void* X, qlora_dtype x_dtype, int64_t ldx,
+                                  const qlora_fp8_matrix* Wq, const qlora_fp8_matrix* Xq, void* Y,
+                                  qlora_dtype y_dtype, int64_t ldy, int* d_status, void* stream);
+qlora_status qlora_fp8_linear_bwd(const void* dY, qlora_dtype dy_dtype, int64_t lddy,
+                                  const qlora_fp8_matrix* Wq, const qlora_fp8_matrix* dYq, void* dX,
+                                  qlora_dtype dx_dtype, int64_t lddx, int* d_status, void* stream);
+
+/*
+ * Layer norm over the rows of X [rows, cols], the norm in front of a frozen
+ * projection (norms stay in 16 bits or more: "QLoRA", scalata.ai, the line
+ * on what is not quantised):
+ *     mean = sum(x) / cols;  rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps)
+ *     y = (x - mean) * rstd * weight + bias
+ * X, Y: `dtype` (fp32 or bf16), ldx / ldy elements between rows; weight,
+ * bias [cols]: w_dtype, either may be NULL (ones, zeros).  mean, rstd: fp32
+ * [rows], each written when non-NULL, for the backward.  Y may be X (same
+ * stride), otherwise they may not overlap.  eps >= 0, finite.  rows = 0 is
+ * a no-op.  Pointers aligned to their element.
+ *
+ * Backward, from the saved mean and rstd:
+ *     xh = (x - mean) * rstd;  g = dy * weight
+ *     dx = rstd * (g - mean(g) - xh * mean(g * xh))
+ *     dweight = sum over rows of dy * xh;  dbias = sum over rows of dy
+ * dweight, dbias [cols]: grad_dtype, overwritten, each skipped when NULL
+ * (a frozen norm passes both NULL and needs no workspace); with rows = 0
+ * they are zeros.  dX may be dY or X (same stride).  Workspace (16-byte
+ * aligned): qlora_layernorm_workspace_bytes(rows, cols), 0 for an invalid
+ * shape or none needed.  Sums and statistics are fp32, outputs are rounded
+ * once; results are deterministic (fixed summation order, no atomics).
+ */
+size_t qlora_layernorm_workspace_bytes(int64_t rows, int64_t cols);
+qlora_status qlora_layernorm_fwd(const void* X, int64_t ldx, int64_t rows, int64_t cols,
+                                 qlora_dtype dtype, const void* weight, const void* bias,
+                                 qlora_dtype w_dtype, float eps, void* Y, int64_t ldy, float* mean,
+                                 float* rstd, void* stream);
+qlora_status qlora_layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx,
+                                 int64_t rows, int64_t cols, qlora_dtype dtype, const void* weight,
+                                 qlora_dtype w_dtype, const float* mean, const float* rstd, void* dX,
+                                 int64_t lddx, void* dweight, void* dbias, qlora_dtype grad_dtype,
+                                 void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Distillation from a teacher's top logits: the loss that a fine-tuning run
+ * against a larger model starts its gradient from.  Row i has student logits
+ * Z[i, 0..vocab) and `top` teacher entries (ids[i, j], t[i, j]):
+ *     p = softmax over the row's listed entries of t / tau
+ *     q = softmax over the vocabulary of z / tau,  lse = log sum exp(z / tau)
+ *     loss[i] = w_i tau^2 sum_j p_j (log p_j - log q[ids_j])
+ *     dZ[i, v] = g_i w_i tau (q_v - sum over j with ids_j = v of p_j)
+ * Z, dZ: `dtype` (fp32 or bf16), ldz / lddz elements between rows, aligned
+ * to their element; ids [rows, top]: int32 (id_bits = 32) or int64 (64); t
+ * [rows, top]: t_dtype fp32 or bf16; w (row_weight) and g (grad_loss): fp32
+ * [rows], NULL = ones; tau > 0, finite; 1 <= top <= 1024; vocab < 2^31.
+ * A negative id marks an unused place; an id >= vocab is left out too and
+ * sets QLORA_DEV_INDEX_BIT.  A teacher logit of -inf has p = 0 and
+ * contributes nothing; an entry with p > 0 at a student logit of -inf makes
+ * the loss +inf.  Each listed place is a term of its own: an id listed twice
+ * counts twice.  A row with w_i = 0 (in the backward also g_i = 0), or with
+ * no entry left, has loss 0 and a gradient of zeros whatever Z holds.  A row
+ * that has entries but no finite logit, a logit of +inf or a NaN, gives NaN.
+ *
+ * fwd: loss fp32 [rows]; lse fp32 [rows], nullable; dZ nullable: when given
+ *   it receives the gradient for g = 1 in the same launch, so that the
+ *   logits are read from memory once.  dZ may be Z (same stride), otherwise
+ *   they may not overlap.
+ * bwd: the gradient from the saved lse.  dZ may be Z (same stride).
+ * rows = 0 is a no-op.  fp32 arithmetic; the gradient is rounded once.
+ * Deterministic.
+ */
+qlora_status qlora_distill_topk_fwd(const void* Z, int64_t ldz, int64_t rows, int64_t vocab,
+                                    qlora_dtype dtype, const void* ids, int id_bits, const void* t,
+                                    qlora_dtype t_dtype, int top, float tau, const float* row_weight,
+                                    float* loss, float* lse, void* dZ, int64_t lddz, int* d_status,
+                                    void* stream);
+qlora_status qlora_distill_topk_bwd(const void* Z, int64_t ldz, int64_t rows, int64_t vocab,
+                                    qlora_dtype dtype, const void* ids, int id_bits, const void* t,
+                                    qlora_dtype t_dtype, int top, float tau, const float* row_weight,
+                                    const float* lse, const float* grad_loss, void* dZ, int64_t lddz,
+                                    int* d_status, void* stream);
 
 /*
  * Test hooks for the bounded device waits (no counterpart on the pages).
