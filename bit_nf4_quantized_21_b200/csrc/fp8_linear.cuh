@@ -12,21 +12,23 @@
 // each block's sum is scaled and added in fp32; the output is rounded once.
 //
 // k_fp8_gemm (many tokens), tensor bound.  A pair of SMs (tcgen05.mma
-// cta_group::2, kind::f8f6f4, M 256 x N 256 x K 32) owns a 256 x 256 output
-// tile; each CTA brings its 128 activation rows and its 128-row half of the
-// weight tile by TMA, 32 KB per block of 128 in a ring of six.  A block's
-// product cannot stay in the tensor core's accumulator (the scales differ
-// from block to block), so each block goes into one of two 256-column
-// accumulators in turn, and eight warps take a finished one out while the
-// next is being computed: acc = fma(D, sx sw, acc) in registers, a row of
-// 128 outputs per thread (sx and sw are one number per thread and block).
-// 256 rows x 256 columns keep that work (one multiply-add per 128 products,
-// packed in pairs) and the operand traffic (64 bytes per clock and SM at the
-// full tensor rate) below the tensor time.  The grid is one pair per two
-// SMs and walks the tiles, so that a tile's output is written while the next
-// one's products are already running.  The same weight bytes serve both
-// directions: a tile of 128 rows x 128 bytes is a K-major operand forward
-// and an MN-major one in dX.
+// cta_group::2, kind::f8f6f4) owns a 256 x 256 output tile; each CTA brings
+// its 128 activation rows and its 128-row half of the weight tile by TMA, 32
+// KB per block of 128 in a ring of six.  A block's product cannot stay in the
+// tensor core's accumulator (the scales differ from block to block): it goes
+// into tensor memory, and eight warps take it out and add it to fp32 sums in
+// registers, acc = fma(D, sx sw, acc), packed in pairs; a thread holds 128
+// outputs of one row, inside one scale block of the weight.  Tensor memory
+// holds two such products and no more, so what bounds the kernel is how fast
+// a place is free again: commit, wake the epilogue, load, tell the leader,
+// issue.  Hence four accumulators of 128 columns instead of two of 256 (a
+// place waits for half as much work), an issuing thread for each (a thread
+// that waits after issuing MMAs stalls until they drain), and the place is
+// handed back as soon as its values are in registers, before they are used.
+// The grid is one pair per two SMs and walks the tiles, so that a tile's
+// output is written while the next one's products are already running.  The
+// same weight bytes serve both directions: a tile of 128 rows x 128 bytes is
+// a K-major operand forward and an MN-major one in dX.
 //
 // k_fp8_gemv (few tokens, forward), HBM bound: the weight streams once from
 // global memory straight into the registers of legacy warp-level MMAs
@@ -290,14 +292,22 @@ __global__ void __launch_bounds__(kF8GemvWarps * 32) k_fp8_gemv(const Fp8GemvArg
 constexpr int kF8Ring = 6;
 constexpr int kF8EpiWarps = 8;
 constexpr int kF8ProdWarp = 8;
-constexpr int kF8IssueWarp = 9;                  // and 10: two issuers
-constexpr int kF8Threads = 32 * 11;
+constexpr int kF8IssueWarp = 9;                  // .. 12: four issuers, one per accumulator
+constexpr int kF8Accs = 4;
+constexpr int kF8Threads = 32 * 16;
+// registers per thread: what the launch gives everyone, then the epilogue's
+// two warpgroups take what the two others hand back
+constexpr int kF8Regs = 128, kF8EpiRegs = 216, kF8RoleRegs = 40;
+static_assert(256 * kF8EpiRegs + 256 * kF8RoleRegs <= kF8Threads * kF8Regs, "register split");
 constexpr uint32_t kF8OpBytes = 128 * 128;       // 16 KB: 128 rows x 128 bytes
 constexpr uint32_t kF8SlotBytes = 2 * kF8OpBytes;
-constexpr uint32_t kF8SmemBytes = kF8Ring * kF8SlotBytes + 1024 /*align*/ + 256 /*bars*/;
+constexpr uint32_t kF8StageBytes = 4096;         // per epilogue warp: 32 rows x 128 bytes of output
+constexpr uint32_t kF8OffStage = kF8Ring * kF8SlotBytes;
+constexpr uint32_t kF8OffBar = kF8OffStage + kF8EpiWarps * kF8StageBytes;
+constexpr uint32_t kF8SmemBytes = kF8OffBar + 1024 /*align*/ + 256 /*bars*/;
 constexpr uint32_t kF8TmemCols = 512;
 constexpr int kF8GroupM = 8;
-static_assert(kF8Ring % 2 == 0, "each slot belongs to one issuer");
+static_assert(kF8Ring % 2 == 0, "an issuer takes every second slot");
 static_assert(kF8SmemBytes <= 227 * 1024, "fp8 GEMM shared memory");
 
 struct Fp8GemmArgs {
@@ -310,7 +320,7 @@ struct Fp8GemmArgs {
   void* out;
   int64_t ldo;
   int out_f32;
-  int out_vec;           // 16-byte stores are aligned for every row
+  int tma_out;           // tm_out maps the output (16-byte aligned rows)
   int tiles_m, tiles_n;
   int* status;
 };
@@ -330,27 +340,23 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int b_mn_major) 
   return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
-// arrive on the barrier of another CTA of the cluster, ordering this
-// thread's earlier accesses before it at cluster scope
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// 32 lanes x 32 bits, 32 consecutive columns per thread
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23,"
+      " %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
 }
-// bounded wait with acquire at cluster scope
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  uint32_t spins = 0;
-  while (true) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((++spins & 63u) == 0) {
-      if (*abort_flag) return false;
-      if (global_ns() - t0 > qlora_wait_limit()) {
-        *abort_flag = 1;
-        if (status) atomicOr(status, QLORA_DEV_TIMEOUT);
-        return false;
-      }
-    }
-  }
+// acc += d * s on two fp32 values at once, each rounded once
+__device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t s2) {
+  asm("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tfma.rn.f32x2 %0, d, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(d0), "r"(d1), "l"(s2));
 }
 
 // output tile t: groups of kF8GroupM tile rows, a group's columns one after
@@ -367,15 +373,15 @@ __device__ __forceinline__ void f8_tile(int t, const Fp8GemmArgs& a, int& tm, in
 template <int MODE>
 __global__ void __launch_bounds__(kF8Threads, 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap tm_act, const __grid_constant__ CUtensorMap tm_w,
-               const Fp8GemmArgs args) {
+               const __grid_constant__ CUtensorMap tm_out, const Fp8GemmArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kF8Ring * kF8SlotBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kF8OffBar);
   uint64_t* full = bars;                         // [ring] leader: both CTAs' tiles landed
-  uint64_t* empty = full + kF8Ring;              // [ring] local: MMA done with the slot
-  uint64_t* acc_full = empty + kF8Ring;          // [2] local: accumulator holds a block's product
-  uint64_t* acc_empty = acc_full + 2;            // [2] leader: both CTAs have taken it out
-  uint64_t* drained = acc_empty + 2;             // local: every MMA issued is done
+  uint64_t* empty = full + kF8Ring;              // [ring] local: both issuers' MMAs done with the slot
+  uint64_t* acc_full = empty + kF8Ring;          // [4] local: accumulator holds its half of a block's product
+  uint64_t* acc_empty = acc_full + kF8Accs;      // [4] leader: both CTAs have taken it out
+  uint64_t* drained = acc_empty + kF8Accs;       // local: every MMA issued is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -386,20 +392,20 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const int tiles = args.tiles_m * args.tiles_n;
   const int KB = static_cast<int>((args.ctr + kF8Block - 1) / kF8Block);
   const int mine = pair < tiles ? (tiles - pair + pairs - 1) / pairs : 0;   // this pair's tiles
-  const int64_t total = static_cast<int64_t>(mine) * KB;                   // blocks over all of them
+  const uint32_t total = static_cast<uint32_t>(mine) * KB;                 // blocks over all of them (host: < 2^31)
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kF8Ring; ++i) { mbar_init(smem_u32(&full[i]), 1); mbar_init(smem_u32(&empty[i]), 1); }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kF8Ring; ++i) { mbar_init(smem_u32(&full[i]), 1); mbar_init(smem_u32(&empty[i]), 2); }
+    for (int i = 0; i < kF8Accs; ++i) {
       mbar_init(smem_u32(&acc_full[i]), 1);
       mbar_init(smem_u32(&acc_empty[i]), 2 * kF8EpiWarps);
     }
-    mbar_init(smem_u32(drained), 2);
+    mbar_init(smem_u32(drained), kF8Accs);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kF8ProdWarp) {
-    if (lane == 0) { tma_prefetch_desc(&tm_act); tma_prefetch_desc(&tm_w); }
+    if (lane == 0) { tma_prefetch_desc(&tm_act); tma_prefetch_desc(&tm_w); tma_prefetch_desc(&tm_out); }
     __syncwarp();
     tmem_alloc_pair(smem_u32(tmem_slot), kF8TmemCols);
     tmem_relinquish_pair();
@@ -411,10 +417,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   auto leader_bar = [&](uint64_t* b) { return mapa_shared(smem_u32(b), 0); };
   if (threadIdx.x == 0) QLORA_CHECK_ONLY(kF8SmemBytes <= dyn_smem_bytes(), 200);
 
-  if (warp == kF8ProdWarp) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int64_t it = 0;
+  if (warp >= kF8EpiWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RoleRegs));
+    if (warp == kF8ProdWarp && lane == 0) {
+      // ---------------------------------------------------------- producer
+      uint32_t it = 0;
       bool live = true;
       for (int t = pair; t < tiles && live; t += pairs) {
         int tm, tn;
@@ -422,9 +429,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         const int32_t m0 = tm * 256 + static_cast<int32_t>(rank) * 128;
         const int32_t c0 = tn * 256 + static_cast<int32_t>(rank) * 128;   // this CTA's half of the output columns
         for (int kb = 0; kb < KB; ++kb, ++it) {
-          const int s = static_cast<int>(it % kF8Ring);
-          if (it >= kF8Ring &&
-              !mbar_wait(smem_u32(&empty[s]), static_cast<uint32_t>((it / kF8Ring + 1) & 1), abort_flag, args.status)) {
+          const uint32_t s = it % kF8Ring;
+          if (it >= kF8Ring && !mbar_wait(smem_u32(&empty[s]), (it / kF8Ring + 1) & 1, abort_flag, args.status)) {
             live = false;
             break;
           }
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           if (leader) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * kF8SlotBytes);
           const uint32_t dst = smem_u32(base) + s * kF8SlotBytes;
           // (a skipped load leaves the slot's wait to run out: bounded, the launch aborts)
-          if (QLORA_CHECK(s >= 0 && (s + 1) * kF8SlotBytes <= kF8Ring * kF8SlotBytes && m0 >= 0 && c0 >= 0, 201)) {
+          if (QLORA_CHECK((s + 1) * kF8SlotBytes <= kF8OffStage && m0 >= 0 && c0 >= 0, 201)) {
             tma_load_2d_pair(dst, &tm_act, fb, kb * kF8Block, m0);
             if (MODE == 0) tma_load_2d_pair(dst + kF8OpBytes, &tm_w, fb, kb * kF8Block, c0);
             else tma_load_2d_pair(dst + kF8OpBytes, &tm_w, fb, c0, kb * kF8Block);
@@ -441,116 +447,149 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       }
       if (*abort_flag && leader) {
         // loads still in flight land before the CTA can exit
-        for (int64_t i = it > kF8Ring ? it - kF8Ring : 0; i < it; ++i) {
+        for (uint32_t i = it > kF8Ring ? it - kF8Ring : 0; i < it; ++i) {
           const uint64_t t1 = global_ns();
-          while (!mbar_try_wait_cluster(smem_u32(&full[i % kF8Ring]), static_cast<uint32_t>((i / kF8Ring) & 1)) &&
+          while (!mbar_try_wait_cluster(smem_u32(&full[i % kF8Ring]), (i / kF8Ring) & 1) &&
                  global_ns() - t1 < qlora_drain_limit()) {}
         }
       }
-    }
-  } else if (warp >= kF8IssueWarp) {
-    // ------------------------------------------------- MMA issuers (leader)
-    // Issuer i takes blocks i, i + 2, ... into accumulator i: a thread that
-    // waits right after issuing stalls until its MMAs drain, so two take turns.
-    if (leader && lane == 0) {
-      const int me = warp - kF8IssueWarp;
-      constexpr uint32_t idesc = idesc_e4m3(256, 256, MODE);
-      const uint32_t dcol = tmem_d + 256u * me;
-      for (int64_t it = me; it < total; it += 2) {
-        const int s = static_cast<int>(it % kF8Ring);
-        const int64_t use = it >> 1;
-        if (use > 0 && !mbar_wait_cluster(smem_u32(&acc_empty[me]), static_cast<uint32_t>((use + 1) & 1), abort_flag, args.status))
-          break;
-        if (!mbar_wait_cluster(smem_u32(&full[s]), static_cast<uint32_t>((it / kF8Ring) & 1), abort_flag, args.status)) break;
+    } else if (warp >= kF8IssueWarp && warp < kF8IssueWarp + kF8Accs && leader && lane == 0) {
+      // --------------------------------------------- MMA issuers (leader)
+      // Issuer j owns accumulator j: half j % 2 of the blocks j / 2, j / 2 +
+      // 2, ...  The half: columns 64 (j % 2) .. of each CTA's 128 weight rows.
+      const uint32_t j = warp - kF8IssueWarp, half = j & 1;
+      constexpr uint32_t idesc = idesc_e4m3(256, 128, MODE);
+      const uint32_t dcol = tmem_d + 128u * j;
+      for (uint32_t it = j >> 1; it < total; it += 2) {
+        const uint32_t s = it % kF8Ring, use = it >> 1;
+        if (use > 0 && !mbar_wait(smem_u32(&acc_empty[j]), (use + 1) & 1, abort_flag, args.status)) break;
+        if (!mbar_wait(smem_u32(&full[s]), (it / kF8Ring) & 1, abort_flag, args.status)) break;
         tc_fence_after();
-        const uint32_t ab = smem_u32(base) + s * kF8SlotBytes, wb = ab + kF8OpBytes;
+        const uint32_t ab = smem_u32(base) + s * kF8SlotBytes, wb = ab + kF8OpBytes + half * (MODE == 0 ? 8192u : 64u);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint64_t adesc = sw128_desc(ab + k * 32, 16, 1024);
           const uint64_t bdesc = MODE == 0 ? sw128_desc(wb + k * 32, 16, 1024) : sw128_desc(wb + k * 4096, 16384, 1024);
           umma_e4m3_pair(dcol, adesc, bdesc, idesc, k > 0 ? 1u : 0u);
         }
+        umma_commit_pair(smem_u32(&acc_full[j]), 0x3);
         umma_commit_pair(smem_u32(&empty[s]), 0x3);
-        umma_commit_pair(smem_u32(&acc_full[me]), 0x3);
       }
       umma_commit_pair(smem_u32(drained), 0x3);
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    // Warp w: rows 32 (w % 4) .. of this CTA, output columns 128 (w / 4) ..
-    const int q = warp & 3, half = warp >> 2;
-    const uint32_t taddr = tmem_d + (static_cast<uint32_t>(q * 32) << 16) + 128u * half;
-    int64_t it = 0;
+    // Warp w: rows 32 (w % 4) .. of this CTA; of each accumulator the 64
+    // columns that come from CTA p = w / 4's weight rows, so that a warp's
+    // 128 output columns 128 p .. lie in one scale block.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8EpiRegs));
+    const int q = warp & 3, p = warp >> 2;
+    const uint32_t taddr = tmem_d + (static_cast<uint32_t>(q * 32) << 16) + 64u * p;
+    const uint32_t freed = leader_bar(&acc_empty[0]);
+    uint8_t* stage = base + kF8OffStage + warp * kF8StageBytes;
+    uint32_t it = 0;
     bool live = true;
     for (int t = pair; t < tiles && live; t += pairs) {
       int tm, tn;
       f8_tile(t, args, tm, tn);
-      const int64_t row = static_cast<int64_t>(tm) * 256 + rank * 128 + q * 32 + lane;
-      const int64_t col = static_cast<int64_t>(tn) * 256 + 128 * half;
+      const int64_t row0 = static_cast<int64_t>(tm) * 256 + rank * 128 + q * 32, row = row0 + lane;
+      const int64_t col = static_cast<int64_t>(tn) * 256 + 128 * p;
       const bool in = row < args.M && col < args.out_cols;
+      // scales of blocks kb, kb + 1, ...: one of the row's, one of the weight's
       const float* sa = args.sa + (in ? row : 0);
       const int64_t ob = in ? col / kF8Block : 0;
-      const float* sw = MODE == 0 ? args.sw + ob * args.sw_cols : args.sw + ob;
       const int64_t sw_step = MODE == 0 ? 1 : args.sw_cols;
-      auto scale_of = [&](int kb) { return kb < KB ? sa[kb * args.M] * sw[kb * sw_step] : 0.0f; };
-      float s0 = scale_of(0), s1 = scale_of(1);
-      float acc[128];
+      const float* sw = MODE == 0 ? args.sw + ob * args.sw_cols : args.sw + ob;
+      float a0 = sa[0], w0 = sw[0], a1 = 0.0f, w1 = 0.0f;
+      if (KB > 1) { a1 = sa[args.M]; w1 = sw[sw_step]; }
+      uint64_t acc[64];
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-      for (int kb = 0; kb < KB; ++kb, ++it) {
-        const int buf = static_cast<int>(it & 1);
-        const float s = s0;
-        s0 = s1;
-        s1 = scale_of(kb + 2);
-        if (!mbar_wait_cluster(smem_u32(&acc_full[buf]), static_cast<uint32_t>((it >> 1) & 1), abort_flag, args.status)) {
-          live = false;
-          break;
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      for (int kb = 0; kb < KB && live; ++kb, ++it) {
+        const float s = a0 * w0;
+        a0 = a1;
+        w0 = w1;
+        sa += args.M;
+        sw += sw_step;
+        if (kb + 2 < KB) { a1 = sa[args.M]; w1 = sw[sw_step]; }   // two blocks ahead
+        uint64_t s2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t buf = 2 * (it & 1) + h;
+          if (!mbar_wait(smem_u32(&acc_full[buf]), (it >> 1) & 1, abort_flag, args.status)) {
+            live = false;
+            break;
+          }
+          __syncwarp();
+          tc_fence_after();
+          uint32_t r[64];
+          tmem_ld32(taddr + 128u * buf, r);
+          tmem_ld32(taddr + 128u * buf + 32, r + 32);
+          tmem_ld_wait();
+          // the product is in registers: the next one may overwrite it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(freed + 8 * buf);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) fma_f32x2(acc[32 * h + i], r[2 * i], r[2 * i + 1], s2);
         }
+      }
+      if (!live) break;
+      // Out through shared memory, 128 bytes of each of the warp's 32 rows at
+      // a time (128-byte swizzle), so that global memory sees whole rows of a
+      // box: by a TMA store, or by the lanes where rows are not 16-byte aligned.
+      const int per = args.out_f32 ? 32 : 64;                      // columns of a box
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (!args.out_f32 && b >= 2) break;
+        if (lane == 0) bulk_wait_read();                           // the box before has been read
         __syncwarp();
-        tc_fence_after();
+        uint8_t* line = stage + lane * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          uint32_t r[16];
-          tmem_ld16(taddr + 256u * buf + 16 * c, r);
-          tmem_ld_wait();
+          uint4 v;
+          if (args.out_f32) {
+            const uint64_t x = acc[16 * b + 2 * c], y = acc[16 * b + 2 * c + 1];
+            v = make_uint4(static_cast<uint32_t>(x), static_cast<uint32_t>(x >> 32), static_cast<uint32_t>(y),
+                           static_cast<uint32_t>(y >> 32));
+          } else {
+            uint32_t pk[4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[16 * c + i] = fmaf(__uint_as_float(r[i]), s, acc[16 * c + i]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_release_cluster(leader_bar(&acc_empty[buf]));
-      }
-      if (live && in) {
-        const int64_t left = args.out_cols - col;
-        if (args.out_f32) {
-          float* dst = static_cast<float*>(args.out) + row * args.ldo + col;
-#pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            if (args.out_vec && c + 4 <= left) {
-              *reinterpret_cast<float4*>(dst + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (c + i < left) dst[c + i] = acc[c + i];
+            for (int i = 0; i < 4; ++i) {
+              const uint64_t x = acc[(32 * b + 4 * c + i) & 63];
+              pk[i] = pack_bf16x2(__uint_as_float(static_cast<uint32_t>(x)), __uint_as_float(static_cast<uint32_t>(x >> 32)));
             }
+            v = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+          *reinterpret_cast<uint4*>(line + ((c ^ (lane & 7)) << 4)) = v;
+        }
+        const int64_t bx = col + b * per;
+        if (args.tma_out) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && bx < args.out_cols && row0 < args.M) {
+            tma_store_2d(&tm_out, smem_u32(stage), static_cast<int32_t>(bx), static_cast<int32_t>(row0));
+            bulk_commit();
           }
         } else {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(args.out) + row * args.ldo + col;
-#pragma unroll
-          for (int c = 0; c < 128; c += 8) {
-            if (args.out_vec && c + 8 <= left) {
-              *reinterpret_cast<uint4*>(dst + c) =
-                  make_uint4(pack_bf16x2(acc[c], acc[c + 1]), pack_bf16x2(acc[c + 2], acc[c + 3]),
-                             pack_bf16x2(acc[c + 4], acc[c + 5]), pack_bf16x2(acc[c + 6], acc[c + 7]));
+          __syncwarp();
+          const int64_t left = args.out_cols - bx;
+          for (int r = 0; r < 32 && row0 + r < args.M; ++r) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+            if (args.out_f32) {
+              if (lane < left) static_cast<float*>(args.out)[(row0 + r) * args.ldo + bx + lane] = __uint_as_float(v);
             } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (c + i < left) dst[c + i] = __float2bfloat16_rn(acc[c + i]);
+              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(args.out) + (row0 + r) * args.ldo + bx + 2 * lane;
+              if (2 * lane < left) dst[0] = __ushort_as_bfloat16(static_cast<uint16_t>(v));
+              if (2 * lane + 1 < left) dst[1] = __ushort_as_bfloat16(static_cast<uint16_t>(v >> 16));
             }
           }
+          __syncwarp();
         }
       }
     }
+    if (lane == 0) bulk_wait_read();   // the stores have read their boxes before the CTA can exit
   }
 
   // Single-lane roles leave their warps diverged; the cluster barrier is

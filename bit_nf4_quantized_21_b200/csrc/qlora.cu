@@ -121,6 +121,12 @@ bool ensure_smem_attrs() {
   ok = ok && cudaFuncSetAttribute(k_gemv_nf4, cudaFuncAttributeMaxDynamicSharedMemorySize, kGvSmemBytes) == cudaSuccess;
   ok = ok && cudaFuncSetAttribute(k_fp8_gemm<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8SmemBytes) == cudaSuccess;
   ok = ok && cudaFuncSetAttribute(k_fp8_gemm<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8SmemBytes) == cudaSuccess;
+  // the FP8 GEMM's warps share out the registers that a launch brings: a
+  // build with fewer would wait for registers that never come
+  for (const void* k : {reinterpret_cast<const void*>(k_fp8_gemm<0>), reinterpret_cast<const void*>(k_fp8_gemm<1>)}) {
+    cudaFuncAttributes fa;
+    ok = ok && cudaFuncGetAttributes(&fa, k) == cudaSuccess && fa.numRegs >= kF8Regs;
+  }
   if (ok) done.fetch_or(bit);
   return ok;
 }
@@ -1334,7 +1340,9 @@ qlora_status run_fp8_gemm(int mode, const qlora_fp8_matrix* Wq, const qlora_fp8_
                           qlora_dtype o_dtype, int64_t ldo, int* status, cudaStream_t cs) {
   const int64_t M = Aq->rows, out_cols = mode == 0 ? Wq->rows : Wq->cols;
   const int64_t tm = cdiv(M, 256), tn = cdiv(out_cols, 256);
-  if (tm * tn > (int64_t(1) << 28)) return QLORA_ERR_UNSUPPORTED;
+  // tiles and a pair's blocks are counted in 32 bits
+  if (tm * tn > (int64_t(1) << 28) || tm * tn * cdiv(mode == 0 ? Wq->cols : Wq->rows, kF8Block) > (int64_t(1) << 30))
+    return QLORA_ERR_UNSUPPORTED;
   if (!ensure_smem_attrs()) return QLORA_ERR_CUDA;
   const int sms = sm_count();
   if (sms < 2) return QLORA_ERR_CUDA;
@@ -1348,7 +1356,15 @@ qlora_status run_fp8_gemm(int mode, const qlora_fp8_matrix* Wq, const qlora_fp8_
   a.M = M; a.out_cols = out_cols; a.ctr = mode == 0 ? Wq->cols : Wq->rows;
   a.sa = Aq->scale; a.sw = Wq->scale; a.sw_cols = cdiv(Wq->cols, kF8Block);
   a.out = out; a.ldo = ldo; a.out_f32 = o_dtype == QLORA_F32 ? 1 : 0;
-  a.out_vec = rows16(out, ldo, dtype_size(o_dtype)) ? 1 : 0;
+  // whole boxes go out by TMA where every output row is 16-byte aligned
+  CUtensorMap to = ta;
+  if (rows16(out, ldo, dtype_size(o_dtype))) {
+    const bool f32 = o_dtype == QLORA_F32;
+    if (!make_map(&to, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, out_cols, M,
+                  static_cast<uint64_t>(ldo) * dtype_size(o_dtype), f32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+      return QLORA_ERR_CUDA;
+    a.tma_out = 1;
+  }
   a.tiles_m = static_cast<int>(tm); a.tiles_n = static_cast<int>(tn);
   a.status = status;
   cudaLaunchConfig_t cfg = {};
@@ -1363,8 +1379,8 @@ qlora_status run_fp8_gemm(int mode, const qlora_fp8_matrix* Wq, const qlora_fp8_
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = mode == 0 ? cudaLaunchKernelEx(&cfg, k_fp8_gemm<0>, ta, tw, a)
-                                  : cudaLaunchKernelEx(&cfg, k_fp8_gemm<1>, ta, tw, a);
+  const cudaError_t e = mode == 0 ? cudaLaunchKernelEx(&cfg, k_fp8_gemm<0>, ta, tw, to, a)
+                                  : cudaLaunchKernelEx(&cfg, k_fp8_gemm<1>, ta, tw, to, a);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return QLORA_ERR_CUDA;

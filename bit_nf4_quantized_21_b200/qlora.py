@@ -87,6 +87,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """Load libqlora.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -534,18 +536,22 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return d
 
 
+# These calls serve single tokens, where a launch takes a few microseconds: the
+# checks below read each property of a tensor once.
+
 def _matrix(t: torch.Tensor, name: str, rows: int | None = None, cols: int | None = None) -> tuple[int, int]:
     """(pointer, elements between rows) of a 2-D tensor whose rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError("libqlora takes CUDA tensors only")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
         raise ValueError(f"{name} must be 2-D [{'rows' if rows is None else rows}, {'cols' if cols is None else cols}]"
-                         f", got {tuple(t.shape)}")
-    n, c = t.shape
-    if c > 1 and t.stride(1) != 1:
+                         f", got {tuple(shape)}")
+    n, c = shape
+    ld, step = t.stride()
+    if step != 1 and c > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    ld = t.stride(0) if n > 1 else c
-    if ld < c:
+    if n <= 1:
+        ld = c
+    elif ld < c:
         raise ValueError(f"{name}: rows overlap")
     return t.data_ptr(), ld
 
@@ -553,9 +559,9 @@ def _matrix(t: torch.Tensor, name: str, rows: int | None = None, cols: int | Non
 def _vector(t: torch.Tensor | None, name: str, n: int, dtype=None) -> int | None:
     if t is None:
         return None
-    if t.numel() != n or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must have {n} elements" + (f" of {dtype}" if dtype is not None else ""))
-    return _ptr(t)
+    if t.numel() != n or (dtype is not None and t.dtype != dtype) or not t.is_contiguous():
+        raise ValueError(f"{name} must have {n} contiguous elements" + (f" of {dtype}" if dtype is not None else ""))
+    return t.data_ptr()
 
 
 _HERE = contextlib.nullcontext()
@@ -564,17 +570,22 @@ _HERE = contextlib.nullcontext()
 def _on(stream, *tensors):
     """The context of a call: its tensors' one device made current, and its
     stream, so that what the call allocates belongs to the stream that uses it."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors of a call must be on one CUDA device")
-    if dev.type != "cuda":
+    dev = tensors[0].get_device()
+    if dev < 0:
         raise ValueError("libqlora takes CUDA tensors only")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors of a call must be on one CUDA device")
     if stream is not None:
-        if stream.device != dev:
+        if stream.device.index != dev:
             raise ValueError("the stream must belong to the tensors' device")
         return torch.cuda.stream(stream)
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _HERE if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+
+
+def _current(t: torch.Tensor) -> int:
+    """The current stream of t's device (current_stream() without its Stream object)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 # ------------------------------------------------------------- FP8 linear layer
@@ -625,7 +636,7 @@ def qlora_fp8_quantize(X: torch.Tensor, out: FP8Matrix | None = None, block_rows
         if out is None:
             out = empty_fp8(X.shape[0], X.shape[1], X.device, block_rows)
         p, ld = _matrix(X, "X", out.rows, out.cols)
-        _check(lib().qlora_fp8_quantize(p, dt, ld, ctypes.byref(out.c()), _ptr(d_status), _stream()),
+        _check(lib().qlora_fp8_quantize(p, dt, ld, ctypes.byref(out.c()), _ptr(d_status), _current(X)),
                "qlora_fp8_quantize")
     return out
 
@@ -646,10 +657,10 @@ def _fp8_linear(where, X, Wq, out, out_dtype, Xq, d_status, stream, in_cols, out
             elif Xq.rows != X.shape[0]:
                 raise ValueError("the scratch must have the activations' rows")
         if out is None:
-            out = torch.empty((Xq.rows, out_cols), dtype=out_dtype, device=Wq.codes.device)
+            out = Xq.codes.new_empty((Xq.rows, out_cols), dtype=out_dtype)
         o, ldo = _matrix(out, "output", Xq.rows, out_cols)
         _check(getattr(lib(), where)(p, dt, ld, ctypes.byref(Wq.c()), ctypes.byref(Xq.c()), o, _dtype(out, "output"),
-                                     ldo, _ptr(d_status), _stream()), where)
+                                     ldo, _ptr(d_status), _current(out)), where)
     return out
 
 
@@ -691,17 +702,17 @@ def qlora_layernorm_fwd(X: torch.Tensor, weight: torch.Tensor | None = None, bia
         rows, cols = X.shape
         (w, b), wdt = _params(cols, weight, bias)
         if Y is None:
-            Y = torch.empty((rows, cols), dtype=X.dtype, device=X.device)
+            Y = torch.empty_like(X, memory_format=torch.contiguous_format)
         elif Y.dtype != X.dtype:
             raise ValueError("Y has X's type")
         y, ldy = _matrix(Y, "Y", rows, cols)
         if mean is None:
-            mean = torch.empty(rows, dtype=torch.float32, device=X.device)
+            mean = X.new_empty(rows, dtype=torch.float32)
         if rstd is None:
-            rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
+            rstd = torch.empty_like(mean)
         _check(lib().qlora_layernorm_fwd(x, ldx, rows, cols, _dtype(X, "X"), w, b, wdt, float(eps), y, ldy,
                                          _vector(mean, "mean", rows, torch.float32),
-                                         _vector(rstd, "rstd", rows, torch.float32), _stream()),
+                                         _vector(rstd, "rstd", rows, torch.float32), _current(X)),
                "qlora_layernorm_fwd")
     return Y, mean, rstd
 
@@ -717,16 +728,16 @@ def qlora_layernorm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor 
         dy, lddy = _matrix(dY, "dY", rows, cols)
         (w,), wdt = _params(cols, weight)
         if dX is None:
-            dX = torch.empty((rows, cols), dtype=X.dtype, device=X.device)
+            dX = torch.empty_like(X, memory_format=torch.contiguous_format)
         if dY.dtype != X.dtype or dX.dtype != X.dtype:
             raise ValueError("dY and dX have X's type")
         dx, lddx = _matrix(dX, "dX", rows, cols)
         if want_params:
             gt = dweight.dtype if dweight is not None else dbias.dtype if dbias is not None else grad_dtype
             if dweight is None:
-                dweight = torch.empty(cols, dtype=gt, device=X.device)
+                dweight = X.new_empty(cols, dtype=gt)
             if dbias is None:
-                dbias = torch.empty(cols, dtype=gt, device=X.device)
+                dbias = torch.empty_like(dweight, dtype=gt)
         gdt = QLORA_F32
         for g in (dweight, dbias):
             if g is not None:
@@ -736,14 +747,13 @@ def qlora_layernorm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor 
         ws, ws_bytes = None, 0
         if dweight is not None or dbias is not None:
             if workspace is None:
-                workspace = torch.empty(max(qlora_layernorm_workspace_bytes(rows, cols), 16), dtype=torch.uint8,
-                                        device=X.device)
+                workspace = X.new_empty(max(qlora_layernorm_workspace_bytes(rows, cols), 16), dtype=torch.uint8)
             ws, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
         _check(lib().qlora_layernorm_bwd(dy, lddy, x, ldx, rows, cols, _dtype(X, "X"), w, wdt,
                                          _vector(mean, "mean", rows, torch.float32),
                                          _vector(rstd, "rstd", rows, torch.float32), dx, lddx,
                                          _vector(dweight, "dweight", cols), _vector(dbias, "dbias", cols), gdt, ws,
-                                         ws_bytes, _stream()), "qlora_layernorm_bwd")
+                                         ws_bytes, _current(X)), "qlora_layernorm_bwd")
     return dX, dweight, dbias
 
 
@@ -776,11 +786,11 @@ def qlora_distill_topk_fwd(Z: torch.Tensor, ids: torch.Tensor, t: torch.Tensor, 
         args, w, d = _distill(Z, ids, t, row_weight, dZ)
         rows = Z.shape[0]
         if loss is None:
-            loss = torch.empty(rows, dtype=torch.float32, device=Z.device)
+            loss = Z.new_empty(rows, dtype=torch.float32)
         if lse is None:
-            lse = torch.empty(rows, dtype=torch.float32, device=Z.device)
+            lse = torch.empty_like(loss)
         _check(lib().qlora_distill_topk_fwd(*args, float(tau), w, _vector(loss, "loss", rows, torch.float32),
-                                            _vector(lse, "lse", rows, torch.float32), *d, _ptr(d_status), _stream()),
+                                            _vector(lse, "lse", rows, torch.float32), *d, _ptr(d_status), _current(Z)),
                "qlora_distill_topk_fwd")
     return loss, lse
 
@@ -792,10 +802,10 @@ def qlora_distill_topk_bwd(Z: torch.Tensor, ids: torch.Tensor, t: torch.Tensor, 
     """The gradient of the losses (weighted by grad_loss) with respect to Z, from the forward's lse."""
     with _on(stream, Z, ids, t, row_weight, lse, grad_loss, dZ, d_status):
         if dZ is None:
-            dZ = torch.empty(Z.shape, dtype=Z.dtype, device=Z.device)
+            dZ = torch.empty_like(Z, memory_format=torch.contiguous_format)
         args, w, d = _distill(Z, ids, t, row_weight, dZ)
         rows = Z.shape[0]
         _check(lib().qlora_distill_topk_bwd(*args, float(tau), w, _vector(lse, "lse", rows, torch.float32),
                                             _vector(grad_loss, "grad_loss", rows, torch.float32), *d, _ptr(d_status),
-                                            _stream()), "qlora_distill_topk_bwd")
+                                            _current(Z)), "qlora_distill_topk_bwd")
     return dZ
