@@ -293,6 +293,7 @@ constexpr int kF8Ring = 6;
 constexpr int kF8EpiWarps = 8;
 constexpr int kF8ProdWarp = 8;
 constexpr int kF8IssueWarp = 9;                  // .. 12: four issuers, one per accumulator
+constexpr int kF8ScaleWarp = 13;
 constexpr int kF8Accs = 4;
 constexpr int kF8Threads = 32 * 16;
 // registers per thread: what the launch gives everyone, then the epilogue's
@@ -303,7 +304,11 @@ constexpr uint32_t kF8OpBytes = 128 * 128;       // 16 KB: 128 rows x 128 bytes
 constexpr uint32_t kF8SlotBytes = 2 * kF8OpBytes;
 constexpr uint32_t kF8StageBytes = 4096;         // per epilogue warp: 32 rows x 128 bytes of output
 constexpr uint32_t kF8OffStage = kF8Ring * kF8SlotBytes;
-constexpr uint32_t kF8OffBar = kF8OffStage + kF8EpiWarps * kF8StageBytes;
+constexpr int kF8ScaleRing = 3;
+constexpr uint32_t kF8ScaleBytes = (128 + 4) * 4; // 128 row scales, the weight's two (and padding)
+constexpr uint32_t kF8OffScale = kF8OffStage + kF8EpiWarps * kF8StageBytes;
+constexpr uint32_t kF8OffBar = kF8OffScale + kF8ScaleRing * kF8ScaleBytes;
+static_assert(kF8OffBar % 8 == 0, "barriers");
 constexpr uint32_t kF8SmemBytes = kF8OffBar + 1024 /*align*/ + 256 /*bars*/;
 constexpr uint32_t kF8TmemCols = 512;
 constexpr int kF8GroupM = 8;
@@ -359,6 +364,24 @@ __device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint32_t d0, uint32_t d
       : "r"(d0), "r"(d1), "l"(s2));
 }
 
+// whether a phase is complete, without waiting
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// one thread of a converged warp, always the same one
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 // output tile t: groups of kF8GroupM tile rows, a group's columns one after
 // the other, so that the tiles in flight share rows and columns in L2
 __device__ __forceinline__ void f8_tile(int t, const Fp8GemmArgs& a, int& tm, int& tn) {
@@ -397,7 +420,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kF8Ring; ++i) { mbar_init(smem_u32(&full[i]), 1); mbar_init(smem_u32(&empty[i]), 2); }
     for (int i = 0; i < kF8Accs; ++i) {
-      mbar_init(smem_u32(&acc_full[i]), 1);
+      mbar_init(smem_u32(&acc_full[i]), i % 2 == 0 ? 2 : 1);      // the first half also brings the block's scales
       mbar_init(smem_u32(&acc_empty[i]), 2 * kF8EpiWarps);
     }
     mbar_init(smem_u32(drained), kF8Accs);
@@ -453,29 +476,81 @@ __global__ void __launch_bounds__(kF8Threads, 1)
                  global_ns() - t1 < qlora_drain_limit()) {}
         }
       }
-    } else if (warp >= kF8IssueWarp && warp < kF8IssueWarp + kF8Accs && leader && lane == 0) {
+    } else if (warp == kF8ScaleWarp) {
+      // ------------------------------------------------------- scale warp
+      // The scales of block `it` (128 rows' and the weight's two) into slot
+      // it % 3, two blocks' loads ahead.  The slot is free: block it - 1 has
+      // been computed, so its accumulator was free before, so the epilogue is
+      // through with block it - 3.  Loads in the epilogue's own warps stalled
+      // its multiply-adds (390 cycles for 64 columns against 150).
+      const int64_t sw_step = MODE == 0 ? 1 : args.sw_cols, sw_run = MODE == 0 ? args.sw_cols : 1;
+      const int64_t runs = (args.out_cols + kF8Block - 1) / kF8Block;
+      uint32_t it = 0;
+      bool live = true;
+      for (int t = pair; t < tiles && live; t += pairs) {
+        int tm, tn;
+        f8_tile(t, args, tm, tn);
+        const int64_t row = static_cast<int64_t>(tm) * 256 + rank * 128 + lane;
+        const int64_t ob = 2 * static_cast<int64_t>(tn) + (lane & 1);
+        const float* sa = args.sa + row;
+        const float* sw = args.sw + (ob < runs ? ob * sw_run : 0);
+        float a[2][4], w[2];
+        auto fetch = [&](int b, int kb) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[b][i] = kb < KB && row + 32 * i < args.M ? sa[kb * args.M + 32 * i] : 0.0f;
+          w[b] = kb < KB ? sw[kb * sw_step] : 0.0f;
+        };
+        fetch(0, 0);
+        fetch(1, 1);
+        for (int kb = 0; kb < KB && live; kb += 2) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            if (kb + b >= KB) break;
+            if (it > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&acc_full[2 * ((it - 1) & 1)]), ((it - 1) >> 1) & 1,
+                                                             abort_flag, args.status))) {
+              live = false;
+              break;
+            }
+            float* slot = reinterpret_cast<float*>(base + kF8OffScale + (it % kF8ScaleRing) * kF8ScaleBytes);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) slot[lane + 32 * i] = a[b][i];
+            if (lane < 2) slot[128 + lane] = w[b];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&acc_full[2 * (it & 1)]));
+            ++it;
+            fetch(b, kb + b + 2);
+          }
+        }
+      }
+    } else if (warp >= kF8IssueWarp && warp < kF8IssueWarp + kF8Accs && leader) {
       // --------------------------------------------- MMA issuers (leader)
       // Issuer j owns accumulator j: half j % 2 of the blocks j / 2, j / 2 +
       // 2, ...  The half: columns 64 (j % 2) .. of each CTA's 128 weight rows.
+      // The whole warp runs the loop, so that the descriptors are uniform
+      // values; one elected thread issues.
       const uint32_t j = warp - kF8IssueWarp, half = j & 1;
       constexpr uint32_t idesc = idesc_e4m3(256, 128, MODE);
       const uint32_t dcol = tmem_d + 128u * j;
       for (uint32_t it = j >> 1; it < total; it += 2) {
         const uint32_t s = it % kF8Ring, use = it >> 1;
-        if (use > 0 && !mbar_wait(smem_u32(&acc_empty[j]), (use + 1) & 1, abort_flag, args.status)) break;
-        if (!mbar_wait(smem_u32(&full[s]), (it / kF8Ring) & 1, abort_flag, args.status)) break;
+        bool ok = mbar_wait(smem_u32(&full[s]), (it / kF8Ring) & 1, abort_flag, args.status);
+        ok = ok && (use == 0 || mbar_wait(smem_u32(&acc_empty[j]), (use + 1) & 1, abort_flag, args.status));
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
         tc_fence_after();
         const uint32_t ab = smem_u32(base) + s * kF8SlotBytes, wb = ab + kF8OpBytes + half * (MODE == 0 ? 8192u : 64u);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t adesc = sw128_desc(ab + k * 32, 16, 1024);
-          const uint64_t bdesc = MODE == 0 ? sw128_desc(wb + k * 32, 16, 1024) : sw128_desc(wb + k * 4096, 16384, 1024);
-          umma_e4m3_pair(dcol, adesc, bdesc, idesc, k > 0 ? 1u : 0u);
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t adesc = sw128_desc(ab + k * 32, 16, 1024);
+            const uint64_t bdesc = MODE == 0 ? sw128_desc(wb + k * 32, 16, 1024) : sw128_desc(wb + k * 4096, 16384, 1024);
+            umma_e4m3_pair(dcol, adesc, bdesc, idesc, k > 0 ? 1u : 0u);
+          }
+          umma_commit_pair(smem_u32(&acc_full[j]), 0x3);
+          umma_commit_pair(smem_u32(&empty[s]), 0x3);
         }
-        umma_commit_pair(smem_u32(&acc_full[j]), 0x3);
-        umma_commit_pair(smem_u32(&empty[s]), 0x3);
+        __syncwarp();
       }
-      umma_commit_pair(smem_u32(drained), 0x3);
+      if (elect_one()) umma_commit_pair(smem_u32(drained), 0x3);
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -485,39 +560,25 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8EpiRegs));
     const int q = warp & 3, p = warp >> 2;
     const uint32_t taddr = tmem_d + (static_cast<uint32_t>(q * 32) << 16) + 64u * p;
-    const uint32_t freed = leader_bar(&acc_empty[0]);
+    const uint32_t freed = leader_bar(&acc_empty[0]), filled = smem_u32(&acc_full[0]);
+    bool ahead = false;
     uint8_t* stage = base + kF8OffStage + warp * kF8StageBytes;
     uint32_t it = 0;
     bool live = true;
     for (int t = pair; t < tiles && live; t += pairs) {
       int tm, tn;
       f8_tile(t, args, tm, tn);
-      const int64_t row0 = static_cast<int64_t>(tm) * 256 + rank * 128 + q * 32, row = row0 + lane;
+      const int64_t row0 = static_cast<int64_t>(tm) * 256 + rank * 128 + q * 32;
       const int64_t col = static_cast<int64_t>(tn) * 256 + 128 * p;
-      const bool in = row < args.M && col < args.out_cols;
-      // scales of blocks kb, kb + 1, ...: one of the row's, one of the weight's
-      const float* sa = args.sa + (in ? row : 0);
-      const int64_t ob = in ? col / kF8Block : 0;
-      const int64_t sw_step = MODE == 0 ? 1 : args.sw_cols;
-      const float* sw = MODE == 0 ? args.sw + ob * args.sw_cols : args.sw + ob;
-      float a0 = sa[0], w0 = sw[0], a1 = 0.0f, w1 = 0.0f;
-      if (KB > 1) { a1 = sa[args.M]; w1 = sw[sw_step]; }
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
       for (int kb = 0; kb < KB && live; ++kb, ++it) {
-        const float s = a0 * w0;
-        a0 = a1;
-        w0 = w1;
-        sa += args.M;
-        sw += sw_step;
-        if (kb + 2 < KB) { a1 = sa[args.M]; w1 = sw[sw_step]; }   // two blocks ahead
-        uint64_t s2;
-        asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+        uint64_t s2 = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t buf = 2 * (it & 1) + h;
-          if (!mbar_wait(smem_u32(&acc_full[buf]), (it >> 1) & 1, abort_flag, args.status)) {
+          if (!ahead && !mbar_wait(filled + 8 * buf, (it >> 1) & 1, abort_flag, args.status)) {
             live = false;
             break;
           }
@@ -527,10 +588,17 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           tmem_ld32(taddr + 128u * buf, r);
           tmem_ld32(taddr + 128u * buf + 32, r + 32);
           tmem_ld_wait();
+          if (h == 0) {
+            const float* slot = reinterpret_cast<const float*>(base + kF8OffScale + (it % kF8ScaleRing) * kF8ScaleBytes);
+            const float s = slot[32 * q + lane] * slot[128 + p];
+            asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+          }
           // the product is in registers: the next one may overwrite it
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(freed + 8 * buf);
+          // whether the next product is there already, asked now and looked at after the additions
+          ahead = mbar_test(filled + 8 * (h == 0 ? buf + 1 : 2 * ((it + 1) & 1)), ((it + h) >> 1) & 1);
 #pragma unroll
           for (int i = 0; i < 32; ++i) fma_f32x2(acc[32 * h + i], r[2 * i], r[2 * i + 1], s2);
         }
