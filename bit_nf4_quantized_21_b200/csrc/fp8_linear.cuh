@@ -32,10 +32,11 @@
 //
 // k_fp8_gemv (few tokens, forward), HBM bound: the weight streams once from
 // global memory straight into the registers of legacy warp-level MMAs
-// (m16n8k32; 16 weight rows x 8 tokens), without shared memory or tensor
-// memory in the way: at M <= 32 the tensor work is 1/100 of what the stream
-// takes, and a warp's fragment loads are whole 64-byte pieces of its rows.
-// Eight warps share a tile's contraction and add their sums in a fixed order.
+// (m16n8k32; 16 weight rows x 8 tokens): at these token counts the tensor
+// work is 1/100 of what the stream takes, and a warp's fragment loads are
+// whole 64-byte pieces of its rows.  The tokens' codes sit in shared memory.
+// Behind the quantiser the kernel is a programmatic dependent launch: its
+// first weights travel while the activations are quantised.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -56,6 +57,14 @@ __device__ __forceinline__ uint32_t f8_pack2(float lo, float hi) {
 __device__ __forceinline__ uint2 f8_pack8(const float (&f)[8], float r) {
   return make_uint2(f8_pack2(f[0] * r, f[1] * r) | (f8_pack2(f[2] * r, f[3] * r) << 16),
                     f8_pack2(f[4] * r, f[5] * r) | (f8_pack2(f[6] * r, f[7] * r) << 16));
+}
+// Largest magnitude as the bits of a float: for magnitudes the order of the
+// bits is the order of the values, and infinities and NaN come out on top.
+__device__ __forceinline__ uint32_t f8_magnitude(const float (&f)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+  return m;
 }
 // scale and reciprocal of a block; a scale below the smallest normal number
 // stands for a block of zeros
@@ -99,45 +108,50 @@ __device__ __forceinline__ void f8_load8(const T* row, int64_t c, int64_t cols, 
 }
 
 // Blocks of 1 x 128: sixteen lanes per block, eight elements each.  HBM
-// bound (reads 2 or 4 bytes, writes 1 per element).  Scales go out
-// block-major ([cols / 128][rows]), the order in which the GEMM's warps, a
-// row per lane, read them.
+// bound (reads 2 or 4 bytes, writes 1 per element).  A CTA takes 16 rows of
+// one block column, so that the scales, which go out block-major ([cols /
+// 128][rows], the order in which the GEMM reads them), leave as one run.
 constexpr int kF8QuantThreads = 256;
+constexpr int kF8QuantRows = kF8QuantThreads / 16;
 template <typename T>
 __global__ void __launch_bounds__(kF8QuantThreads) k_fp8_quant_rows(const Fp8QuantArgs a) {
-  const int64_t blocks = (a.cols + kF8Block - 1) / kF8Block;
-  const int64_t g = (static_cast<int64_t>(blockIdx.x) * kF8QuantThreads + threadIdx.x) >> 4;
-  if (g < a.rows * blocks) {
-    const int64_t row = g / blocks, kb = g % blocks;
-    const int64_t c = kb * kF8Block + (threadIdx.x & 15) * 8;
-    float f[8];
-    f8_load8(static_cast<const T*>(a.x) + row * a.ldx, c, a.cols, a.vec, f);
-    float m = 0.0f;
-    bool bad = false;
+  __shared__ float scales[kF8QuantRows];
+  griddep_launch_dependents();            // the product behind may bring its weights meanwhile
+  const uint32_t blocks = static_cast<uint32_t>((a.cols + kF8Block - 1) / kF8Block);
+  const uint32_t kb = blockIdx.x % blocks;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / blocks) * kF8QuantRows;
+  const int r = threadIdx.x >> 4;
+  const int64_t row = row0 + r, c = static_cast<int64_t>(kb) * kF8Block + (threadIdx.x & 15) * 8;
+  const bool in = row < a.rows && c < a.cols;
+  float f[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { m = fmaxf(m, fabsf(f[i])); bad |= !isfinite(f[i]); }
-    const uint32_t half = 0xFFFFu << (threadIdx.x & 16);   // the other half-warp's block may lie past the end
+  for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+  if (in) f8_load8(static_cast<const T*>(a.x) + row * a.ldx, c, a.cols, a.vec, f);
+  uint32_t m = f8_magnitude(f);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, o));
-    float s, r;
-    f8_scale(m, s, r);
-    if (c < a.cols) *reinterpret_cast<uint2*>(a.codes + row * a.ldq + c) = f8_pack8(f, r);
-    if ((threadIdx.x & 15) == 0) a.scale[kb * a.rows + row] = s;
-    if (bad && a.status) atomicOr(a.status, QLORA_DEV_NONFINITE);
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  float s, rc;
+  f8_scale(__uint_as_float(m), s, rc);
+  if (in) *reinterpret_cast<uint2*>(a.codes + row * a.ldq + c) = f8_pack8(f, rc);
+  if ((threadIdx.x & 15) == 0) {
+    scales[r] = s;
+    if (m >= 0x7F800000u && a.status) atomicOr(a.status, QLORA_DEV_NONFINITE);
   }
+  __syncthreads();
+  if (threadIdx.x < kF8QuantRows && row0 + threadIdx.x < a.rows)
+    a.scale[static_cast<int64_t>(kb) * a.rows + row0 + threadIdx.x] = scales[threadIdx.x];
 }
 
 // Blocks of 128 x 128: one CTA per block, 64 elements per thread in registers.
 template <typename T>
 __global__ void __launch_bounds__(256) k_fp8_quant_blocks(const Fp8QuantArgs a) {
-  __shared__ float red[8];
+  __shared__ uint32_t red[8];
   const int64_t nkb = (a.cols + kF8Block - 1) / kF8Block;
   const int64_t nb = blockIdx.x / nkb, kb = blockIdx.x % nkb;
   const int64_t c = kb * kF8Block + (threadIdx.x & 15) * 8;
   const int64_t r0 = nb * kF8Block + (threadIdx.x >> 4);
   float f[8][8];
-  float m = 0.0f;
-  bool bad = false;
+  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t row = r0 + 16 * i;
@@ -147,24 +161,25 @@ __global__ void __launch_bounds__(256) k_fp8_quant_blocks(const Fp8QuantArgs a) 
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[i][e] = 0.0f;
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) { m = fmaxf(m, fabsf(f[i][e])); bad |= !isfinite(f[i][e]); }
+    m = max(m, f8_magnitude(f[i]));
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, red[i]);
+  for (int i = 0; i < 8; ++i) m = max(m, red[i]);
   float s, r;
-  f8_scale(m, s, r);
+  f8_scale(__uint_as_float(m), s, r);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t row = r0 + 16 * i;
     if (row < a.rows && c < a.cols) *reinterpret_cast<uint2*>(a.codes + row * a.ldq + c) = f8_pack8(f[i], r);
   }
-  if (threadIdx.x == 0) a.scale[nb * nkb + kb] = s;
-  if (bad && a.status) atomicOr(a.status, QLORA_DEV_NONFINITE);
+  if (threadIdx.x == 0) {
+    a.scale[nb * nkb + kb] = s;
+    if (m >= 0x7F800000u && a.status) atomicOr(a.status, QLORA_DEV_NONFINITE);
+  }
 }
 
 // --------------------------------------------------- few tokens: the stream
@@ -179,6 +194,7 @@ struct Fp8GemvArgs {
   void* y;
   int64_t ldy;
   int y_f32;
+  int after_quant;       // launched as a dependent of the quantiser
 };
 
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -208,82 +224,164 @@ __device__ __forceinline__ uint4 f8_bytes16(const uint8_t* row, int64_t k, int64
   return v;
 }
 
-constexpr int kF8GemvWarps = 8;
+constexpr int kF8GemvWarps = 16;
+constexpr int kF8GemvThreads = 32 * kF8GemvWarps;
 constexpr int kF8GemvRows = 16;
 
+// Shared memory of a launch: the tokens' codes (rows `xs` bytes apart: 64
+// more than a multiple of 128, so that the eight rows that a load takes lie
+// in different banks), their scales, the warps' sums of one tile.
+struct Fp8GemvSmem {
+  uint32_t xs, off_scale, off_part, bytes;
+};
+__host__ __device__ inline Fp8GemvSmem fp8_gemv_smem(int M, int64_t K, int nt) {
+  Fp8GemvSmem s;
+  const uint32_t blocks = static_cast<uint32_t>((K + kF8Block - 1) / kF8Block);
+  s.xs = blocks * kF8Block + 64;
+  s.off_scale = s.xs * static_cast<uint32_t>(M);
+  s.off_part = s.off_scale + blocks * nt * 8 * 4;
+  s.bytes = s.off_part + kF8GemvWarps * kF8GemvRows * (nt * 8 + 1) * 4;
+  return s;
+}
+
+// A weight load: read once, kept out of L1
+__device__ __forceinline__ uint4 f8_stream16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// One CTA per SM.  Its tiles of 16 weight rows are shared out by blocks of the
+// contraction: warp w takes blocks w, w + 16, ...; every warp has two blocks'
+// weights on their way (32 x 64 bytes each), across the end of a tile too.
 // The contraction's order inside a block is free as long as both operands
 // follow it: lane quad c holds bytes 16c .. 16c + 15 and 64 + 16c .. of each
 // of its rows, and MMA i takes 8 of them.
 template <int NT>
-__global__ void __launch_bounds__(kF8GemvWarps * 32) k_fp8_gemv(const Fp8GemvArgs a) {
-  __shared__ float part[kF8GemvWarps][kF8GemvRows][NT * 8 + 1];
+__global__ void __launch_bounds__(kF8GemvThreads, 1) k_fp8_gemv(const Fp8GemvArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const Fp8GemvSmem lay = fp8_gemv_smem(a.M, a.K, NT);
+  float* sxs = reinterpret_cast<float*>(smem_raw + lay.off_scale);      // [block][NT * 8]
+  float* part = reinterpret_cast<float*>(smem_raw + lay.off_part);      // [warp][row][NT * 8 + 1]
+  constexpr int kPitch = NT * 8 + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kF8GemvRows;
-  const int64_t blocks = (a.K + kF8Block - 1) / kF8Block;
-  const uint8_t* w0 = a.w + min(n0 + g, a.N - 1) * a.ldw;
-  const uint8_t* w1 = a.w + min(n0 + g + 8, a.N - 1) * a.ldw;
-  const float* sw = a.sw + (n0 / kF8Block) * blocks;
+  const int blocks = static_cast<int>((a.K + kF8Block - 1) / kF8Block);
+  const int tiles = static_cast<int>((a.N + kF8GemvRows - 1) / kF8GemvRows);
+  const int grid = static_cast<int>(gridDim.x);
+  const bool busy = warp < blocks;
+
+  uint4 buf[2][4];
+  float bsw[2];
+  int pt = blockIdx.x, pk = warp;            // the next block to fetch
+  auto fetch = [&](uint4 (&v)[4], float& s) {
+    if (busy && pt < tiles) {
+      const int64_t n0 = static_cast<int64_t>(pt) * kF8GemvRows;
+      const uint8_t* w0 = a.w + min(n0 + g, a.N - 1) * a.ldw;
+      const uint8_t* w1 = a.w + min(n0 + g + 8, a.N - 1) * a.ldw;
+      const int64_t k = static_cast<int64_t>(pk) * kF8Block + 16 * c;
+      if (static_cast<int64_t>(pk + 1) * kF8Block <= a.K) {
+        v[0] = f8_stream16(w0 + k);
+        v[1] = f8_stream16(w1 + k);
+        v[2] = f8_stream16(w0 + k + 64);
+        v[3] = f8_stream16(w1 + k + 64);
+      } else {                               // bytes past the last column may hold anything
+        v[0] = f8_bytes16(w0, k, a.K);
+        v[1] = f8_bytes16(w1, k, a.K);
+        v[2] = f8_bytes16(w0, k + 64, a.K);
+        v[3] = f8_bytes16(w1, k + 64, a.K);
+      }
+      s = a.sw[n0 / kF8Block * blocks + pk];
+      pk += kF8GemvWarps;
+      if (pk >= blocks) { pk = warp; pt += grid; }
+    }
+  };
+  fetch(buf[0], bsw[0]);
+  fetch(buf[1], bsw[1]);
+  if (a.after_quant) griddep_wait();         // the activations come from the kernel ahead, the weights do not
+  for (int i = threadIdx.x; i < a.M * blocks * 8; i += kF8GemvThreads) {
+    const int tok = i / (blocks * 8);
+    const int64_t k = static_cast<int64_t>(i % (blocks * 8)) * 16;
+    *reinterpret_cast<uint4*>(smem_raw + tok * lay.xs + k) = f8_bytes16(a.x + tok * a.ldx, k, a.K);
+  }
+  for (int i = threadIdx.x; i < blocks * NT * 8; i += kF8GemvThreads) {
+    const int tok = i % (NT * 8);
+    sxs[i] = tok < a.M ? a.sx[static_cast<int64_t>(i / (NT * 8)) * a.M + tok] : 0.0f;
+  }
+  __syncthreads();
+
   float acc[NT][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
-
-  uint4 next[4];
-  float nsw = 0.0f;
-  auto fetch = [&](int64_t kb) {
-    const int64_t k = kb * kF8Block + 16 * c;
-    next[0] = f8_bytes16(w0, k, a.K);
-    next[1] = f8_bytes16(w1, k, a.K);
-    next[2] = f8_bytes16(w0, k + 64, a.K);
-    next[3] = f8_bytes16(w1, k + 64, a.K);
-    nsw = sw[kb];
-  };
-  if (warp < blocks) fetch(warp);
-  for (int64_t kb = warp; kb < blocks; kb += kF8GemvWarps) {
-    const uint4 p0 = next[0], q0 = next[1], p1 = next[2], q1 = next[3];
-    const float s = nsw;
-    if (kb + kF8GemvWarps < blocks) fetch(kb + kF8GemvWarps);
-    const int64_t k = kb * kF8Block + 16 * c;
+  // the tile's sums over the warps, in warp order
+  auto finish = [&](int tile) {
+    float* mine = part + warp * kF8GemvRows * kPitch;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int tok = t * 8 + g;
-      uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-      if (tok < a.M) {
-        x0 = f8_bytes16(a.x + tok * a.ldx, k, a.K);
-        x1 = f8_bytes16(a.x + tok * a.ldx, k + 64, a.K);
-      }
-      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      mma_e4m3(d, p0.x, q0.x, p0.y, q0.y, x0.x, x0.y);
-      mma_e4m3(d, p0.z, q0.z, p0.w, q0.w, x0.z, x0.w);
-      mma_e4m3(d, p1.x, q1.x, p1.y, q1.y, x1.x, x1.y);
-      mma_e4m3(d, p1.z, q1.z, p1.w, q1.w, x1.z, x1.w);
-      const int t0 = t * 8 + 2 * c;
-      const float s0 = t0 < a.M ? s * a.sx[kb * a.M + t0] : 0.0f;
-      const float s1 = t0 + 1 < a.M ? s * a.sx[kb * a.M + t0 + 1] : 0.0f;
-      acc[t][0] = fmaf(d[0], s0, acc[t][0]);
-      acc[t][1] = fmaf(d[1], s1, acc[t][1]);
-      acc[t][2] = fmaf(d[2], s0, acc[t][2]);
-      acc[t][3] = fmaf(d[3], s1, acc[t][3]);
+      mine[g * kPitch + t * 8 + 2 * c] = acc[t][0];
+      mine[g * kPitch + t * 8 + 2 * c + 1] = acc[t][1];
+      mine[(g + 8) * kPitch + t * 8 + 2 * c] = acc[t][2];
+      mine[(g + 8) * kPitch + t * 8 + 2 * c + 1] = acc[t][3];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
     }
-  }
+    __syncthreads();
+    const int64_t n0 = static_cast<int64_t>(tile) * kF8GemvRows;
+    for (int i = threadIdx.x; i < kF8GemvRows * NT * 8; i += kF8GemvThreads) {
+      const int r = i % kF8GemvRows, tok = i / kF8GemvRows;
+      if (tok < a.M && n0 + r < a.N) {
+        float s = 0.0f;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    part[warp][g][t * 8 + 2 * c] = acc[t][0];
-    part[warp][g][t * 8 + 2 * c + 1] = acc[t][1];
-    part[warp][g + 8][t * 8 + 2 * c] = acc[t][2];
-    part[warp][g + 8][t * 8 + 2 * c + 1] = acc[t][3];
+        for (int k = 0; k < kF8GemvWarps; ++k) s += part[(k * kF8GemvRows + r) * kPitch + tok];
+        const int64_t at = tok * a.ldy + n0 + r;
+        if (a.y_f32) static_cast<float*>(a.y)[at] = s;
+        else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(s);
+      }
+    }
+    __syncthreads();
+  };
+  if (!busy) {                               // fewer blocks than warps: zeros to every sum
+    for (int tile = blockIdx.x; tile < tiles; tile += grid) finish(tile);
+    return;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kF8GemvRows * NT * 8; i += kF8GemvWarps * 32) {
-    const int r = i % kF8GemvRows, tok = i / kF8GemvRows;
-    if (tok < a.M && n0 + r < a.N) {
-      float s = part[0][r][tok];
+  int tile = blockIdx.x, kb = warp;
+  while (tile < tiles) {
 #pragma unroll
-      for (int k = 1; k < kF8GemvWarps; ++k) s += part[k][r][tok];
-      const int64_t at = tok * a.ldy + n0 + r;
-      if (a.y_f32) static_cast<float*>(a.y)[at] = s;
-      else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(s);
+    for (int b = 0; b < 2; ++b) {
+      if (tile >= tiles) break;
+      const uint4 p0 = buf[b][0], q0 = buf[b][1], p1 = buf[b][2], q1 = buf[b][3];
+      const float s = bsw[b];
+      const uint8_t* xk = smem_raw + kb * kF8Block + 16 * c;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int tok = t * 8 + g;
+        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+        if (tok < a.M) {
+          x0 = *reinterpret_cast<const uint4*>(xk + tok * lay.xs);
+          x1 = *reinterpret_cast<const uint4*>(xk + tok * lay.xs + 64);
+        }
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        mma_e4m3(d, p0.x, q0.x, p0.y, q0.y, x0.x, x0.y);
+        mma_e4m3(d, p0.z, q0.z, p0.w, q0.w, x0.z, x0.w);
+        mma_e4m3(d, p1.x, q1.x, p1.y, q1.y, x1.x, x1.y);
+        mma_e4m3(d, p1.z, q1.z, p1.w, q1.w, x1.z, x1.w);
+        const float2 sx = *reinterpret_cast<const float2*>(sxs + kb * (NT * 8) + t * 8 + 2 * c);
+        const float s0 = s * sx.x, s1 = s * sx.y;
+        acc[t][0] = fmaf(d[0], s0, acc[t][0]);
+        acc[t][1] = fmaf(d[1], s1, acc[t][1]);
+        acc[t][2] = fmaf(d[2], s0, acc[t][2]);
+        acc[t][3] = fmaf(d[3], s1, acc[t][3]);
+      }
+      fetch(buf[b], bsw[b]);
+      kb += kF8GemvWarps;
+      if (kb >= blocks) {
+        finish(tile);
+        kb = warp;
+        tile += grid;
+      }
     }
   }
 }
@@ -327,6 +425,7 @@ struct Fp8GemmArgs {
   int out_f32;
   int tma_out;           // tm_out maps the output (16-byte aligned rows)
   int tiles_m, tiles_n;
+  int after_quant;       // launched as a dependent of the quantiser
   int* status;
 };
 
@@ -446,6 +545,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       // ---------------------------------------------------------- producer
       uint32_t it = 0;
       bool live = true;
+      bool waiting = args.after_quant;   // for the activations: they come from the kernel ahead
       for (int t = pair; t < tiles && live; t += pairs) {
         int tm, tn;
         f8_tile(t, args, tm, tn);
@@ -462,9 +562,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           const uint32_t dst = smem_u32(base) + s * kF8SlotBytes;
           // (a skipped load leaves the slot's wait to run out: bounded, the launch aborts)
           if (QLORA_CHECK((s + 1) * kF8SlotBytes <= kF8OffStage && m0 >= 0 && c0 >= 0, 201)) {
-            tma_load_2d_pair(dst, &tm_act, fb, kb * kF8Block, m0);
             if (MODE == 0) tma_load_2d_pair(dst + kF8OpBytes, &tm_w, fb, kb * kF8Block, c0);
             else tma_load_2d_pair(dst + kF8OpBytes, &tm_w, fb, c0, kb * kF8Block);
+            if (waiting) { griddep_wait(); waiting = false; }
+            tma_load_2d_pair(dst, &tm_act, fb, kb * kF8Block, m0);
           }
         }
       }
@@ -485,6 +586,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       // its multiply-adds (390 cycles for 64 columns against 150).
       const int64_t sw_step = MODE == 0 ? 1 : args.sw_cols, sw_run = MODE == 0 ? args.sw_cols : 1;
       const int64_t runs = (args.out_cols + kF8Block - 1) / kF8Block;
+      if (args.after_quant) griddep_wait();
       uint32_t it = 0;
       bool live = true;
       for (int t = pair; t < tiles && live; t += pairs) {

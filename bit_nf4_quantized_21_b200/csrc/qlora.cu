@@ -121,6 +121,9 @@ bool ensure_smem_attrs() {
   ok = ok && cudaFuncSetAttribute(k_gemv_nf4, cudaFuncAttributeMaxDynamicSharedMemorySize, kGvSmemBytes) == cudaSuccess;
   ok = ok && cudaFuncSetAttribute(k_fp8_gemm<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8SmemBytes) == cudaSuccess;
   ok = ok && cudaFuncSetAttribute(k_fp8_gemm<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8SmemBytes) == cudaSuccess;
+  for (const void* k : {reinterpret_cast<const void*>(k_fp8_gemv<1>), reinterpret_cast<const void*>(k_fp8_gemv<2>),
+                        reinterpret_cast<const void*>(k_fp8_gemv<4>)})
+    ok = ok && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) == cudaSuccess;
   // the FP8 GEMM's warps share out the registers that a launch brings: a
   // build with fewer would wait for registers that never come
   for (const void* k : {reinterpret_cast<const void*>(k_fp8_gemm<0>), reinterpret_cast<const void*>(k_fp8_gemm<1>)}) {
@@ -1307,7 +1310,7 @@ qlora_status run_fp8_quantize(const void* X, qlora_dtype dt, int64_t ldx, const 
   a.status = status;
   const int64_t kb = cdiv(out->cols, kF8Block);
   if (out->block_rows == 1) {
-    const int64_t grid = cdiv(out->rows * kb * 16, kF8QuantThreads);
+    const int64_t grid = cdiv(out->rows, kF8QuantRows) * kb;
     if (grid > 0x7FFFFFFF) return QLORA_ERR_UNSUPPORTED;
     if (dt == QLORA_BF16) k_fp8_quant_rows<__nv_bfloat16><<<static_cast<unsigned>(grid), kF8QuantThreads, 0, cs>>>(a);
     else k_fp8_quant_rows<float><<<static_cast<unsigned>(grid), kF8QuantThreads, 0, cs>>>(a);
@@ -1320,24 +1323,58 @@ qlora_status run_fp8_quantize(const void* X, qlora_dtype dt, int64_t ldx, const 
   return check_launch();
 }
 
-// Token counts up to this take the weight-streaming kernel in the forward.
+// Up to this many tokens, and as long as their codes fit in shared memory,
+// the forward takes the weight-streaming kernel.
 constexpr int64_t kF8GemvMaxM = 32;
+constexpr uint32_t kF8GemvMaxSmem = 227 * 1024;
+int fp8_gemv_nt(int64_t M) { return M <= 8 ? 1 : M <= 16 ? 2 : 4; }
+bool fp8_takes_gemv(int64_t M, int64_t K) {
+  return M <= kF8GemvMaxM && K < (int64_t(1) << 20) &&
+         fp8_gemv_smem(static_cast<int>(M), K, fp8_gemv_nt(M)).bytes <= kF8GemvMaxSmem;
+}
+
+// Launch attributes: a cluster of `cluster` CTAs, and, behind the quantiser,
+// a programmatic dependent launch.
+struct LaunchAttrs {
+  cudaLaunchAttribute a[2];
+  LaunchAttrs(cudaLaunchConfig_t& cfg, int cluster, bool dependent) {
+    a[0].id = cudaLaunchAttributeClusterDimension;
+    a[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    a[0].val.clusterDim.y = 1;
+    a[0].val.clusterDim.z = 1;
+    a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = a;
+    cfg.numAttrs = dependent ? 2 : 1;
+  }
+};
 
 qlora_status run_fp8_gemv(const qlora_fp8_matrix* Wq, const qlora_fp8_matrix* Xq, void* Y, qlora_dtype y_dtype,
-                          int64_t ldy, cudaStream_t cs) {
+                          int64_t ldy, bool after_quant, cudaStream_t cs) {
   Fp8GemvArgs a{};
   a.w = Wq->codes; a.ldw = Wq->ld; a.N = Wq->rows; a.K = Wq->cols; a.sw = Wq->scale;
   a.x = Xq->codes; a.ldx = Xq->ld; a.M = static_cast<int>(Xq->rows); a.sx = Xq->scale;
   a.y = Y; a.ldy = ldy; a.y_f32 = y_dtype == QLORA_F32 ? 1 : 0;
-  const unsigned grid = static_cast<unsigned>(cdiv(a.N, kF8GemvRows));
-  if (a.M <= 8) k_fp8_gemv<1><<<grid, kF8GemvWarps * 32, 0, cs>>>(a);
-  else if (a.M <= 16) k_fp8_gemv<2><<<grid, kF8GemvWarps * 32, 0, cs>>>(a);
-  else k_fp8_gemv<4><<<grid, kF8GemvWarps * 32, 0, cs>>>(a);
-  return check_launch();
+  a.after_quant = after_quant ? 1 : 0;
+  if (!ensure_smem_attrs()) return QLORA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(std::max(1, sm_count()), cdiv(a.N, kF8GemvRows))));
+  cfg.blockDim = dim3(kF8GemvThreads);
+  cfg.dynamicSmemBytes = fp8_gemv_smem(a.M, a.K, fp8_gemv_nt(a.M)).bytes;
+  cfg.stream = cs;
+  LaunchAttrs attrs(cfg, 1, after_quant);
+  const cudaError_t e = a.M <= 8    ? cudaLaunchKernelEx(&cfg, k_fp8_gemv<1>, a)
+                        : a.M <= 16 ? cudaLaunchKernelEx(&cfg, k_fp8_gemv<2>, a)
+                                    : cudaLaunchKernelEx(&cfg, k_fp8_gemv<4>, a);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return QLORA_ERR_CUDA;
+  }
+  return QLORA_OK;
 }
 
 qlora_status run_fp8_gemm(int mode, const qlora_fp8_matrix* Wq, const qlora_fp8_matrix* Aq, void* out,
-                          qlora_dtype o_dtype, int64_t ldo, int* status, cudaStream_t cs) {
+                          qlora_dtype o_dtype, int64_t ldo, bool after_quant, int* status, cudaStream_t cs) {
   const int64_t M = Aq->rows, out_cols = mode == 0 ? Wq->rows : Wq->cols;
   const int64_t tm = cdiv(M, 256), tn = cdiv(out_cols, 256);
   // tiles and a pair's blocks are counted in 32 bits
@@ -1372,13 +1409,8 @@ qlora_status run_fp8_gemm(int mode, const qlora_fp8_matrix* Wq, const qlora_fp8_
   cfg.blockDim = dim3(kF8Threads);
   cfg.dynamicSmemBytes = kF8SmemBytes;
   cfg.stream = cs;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  a.after_quant = after_quant ? 1 : 0;
+  LaunchAttrs attrs(cfg, 2, after_quant);
   const cudaError_t e = mode == 0 ? cudaLaunchKernelEx(&cfg, k_fp8_gemm<0>, ta, tw, to, a)
                                   : cudaLaunchKernelEx(&cfg, k_fp8_gemm<1>, ta, tw, to, a);
   if (e != cudaSuccess) {
@@ -1406,8 +1438,8 @@ qlora_status fp8_linear(int mode, const void* X, qlora_dtype x_dtype, int64_t ld
     st = run_fp8_quantize(X, x_dtype, ldx, Xq, status, cs);
     if (st != QLORA_OK) return st;
   }
-  if (mode == 0 && Xq->rows <= kF8GemvMaxM) return run_fp8_gemv(Wq, Xq, Y, y_dtype, ldy, cs);
-  return run_fp8_gemm(mode, Wq, Xq, Y, y_dtype, ldy, status, cs);
+  if (mode == 0 && fp8_takes_gemv(Xq->rows, Xq->cols)) return run_fp8_gemv(Wq, Xq, Y, y_dtype, ldy, X != nullptr, cs);
+  return run_fp8_gemm(mode, Wq, Xq, Y, y_dtype, ldy, X != nullptr, status, cs);
 }
 
 }  // namespace
