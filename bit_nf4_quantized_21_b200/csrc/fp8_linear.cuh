@@ -254,8 +254,8 @@ __device__ __forceinline__ uint4 f8_stream16(const uint8_t* p) {
 }
 
 // One CTA per SM.  Its tiles of 16 weight rows are shared out by blocks of the
-// contraction: warp w takes blocks w, w + 16, ...; every warp has two blocks'
-// weights on their way (32 x 64 bytes each), across the end of a tile too.
+// contraction: warp w takes blocks w, w + 16, ...; every warp has the weights
+// of a few blocks on their way (2 KB each), across the end of a tile too.
 // The contraction's order inside a block is free as long as both operands
 // follow it: lane quad c holds bytes 16c .. 16c + 15 and 64 + 16c .. of each
 // of its rows, and MMA i takes 8 of them.
@@ -272,8 +272,9 @@ __global__ void __launch_bounds__(kF8GemvThreads, 1) k_fp8_gemv(const Fp8GemvArg
   const int grid = static_cast<int>(gridDim.x);
   const bool busy = warp < blocks;
 
-  uint4 buf[2][4];
-  float bsw[2];
+  constexpr int kAhead = NT == 1 ? 4 : NT == 2 ? 3 : 2;      // blocks on their way (as many as registers hold)
+  uint4 buf[kAhead][4];
+  float bsw[kAhead];
   int pt = blockIdx.x, pk = warp;            // the next block to fetch
   auto fetch = [&](uint4 (&v)[4], float& s) {
     if (busy && pt < tiles) {
@@ -297,8 +298,8 @@ __global__ void __launch_bounds__(kF8GemvThreads, 1) k_fp8_gemv(const Fp8GemvArg
       if (pk >= blocks) { pk = warp; pt += grid; }
     }
   };
-  fetch(buf[0], bsw[0]);
-  fetch(buf[1], bsw[1]);
+#pragma unroll
+  for (int b = 0; b < kAhead; ++b) fetch(buf[b], bsw[b]);
   if (a.after_quant) griddep_wait();         // the activations come from the kernel ahead, the weights do not
   for (int i = threadIdx.x; i < a.M * blocks * 8; i += kF8GemvThreads) {
     const int tok = i / (blocks * 8);
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kF8GemvThreads, 1) k_fp8_gemv(const Fp8GemvArg
   int tile = blockIdx.x, kb = warp;
   while (tile < tiles) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAhead; ++b) {
       if (tile >= tiles) break;
       const uint4 p0 = buf[b][0], q0 = buf[b][1], p1 = buf[b][2], q1 = buf[b][3];
       const float s = bsw[b];
