@@ -50,6 +50,8 @@ struct LnArgs {
   void* dx;
   int64_t lddx;
   float* part;          // [parts][2][cols] partials of dw, db; null: not wanted
+  int stages;           // ring kernels: rows in shared memory
+  int* status;
 };
 
 template <typename T> struct LnElem;
@@ -245,6 +247,32 @@ __global__ void __launch_bounds__(kLnStreamThreads) k_ln_fwd_stream(const LnArgs
   }
 }
 
+// One group's sums of dw and db as row `group` of the partials.
+template <int VEC, int GROUP, int PER>
+__device__ __forceinline__ void ln_write_part(const LnArgs& a, int64_t group, int t, const float (&dw)[PER][VEC],
+                                              const float (&db)[PER][VEC]) {
+  float* pw = a.part + group * 2 * a.cols;
+  float* pb = pw + a.cols;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
+    if (c < a.cols) {
+      if (VEC == 1) {
+        pw[c] = dw[i][0];
+        pb[c] = db[i][0];
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+          *reinterpret_cast<float4*>(pw + c + e) =
+              make_float4(dw[i][e], dw[i][(e + 1) % VEC], dw[i][(e + 2) % VEC], dw[i][(e + 3) % VEC]);
+          *reinterpret_cast<float4*>(pb + c + e) =
+              make_float4(db[i][e], db[i][(e + 1) % VEC], db[i][(e + 2) % VEC], db[i][(e + 3) % VEC]);
+        }
+      }
+    }
+  }
+}
+
 // Backward, rows in registers.  The grid walks the rows; the loads of the
 // next row are in flight while the current one is reduced.
 template <typename T, int VEC, int GROUP, int PER>
@@ -323,28 +351,201 @@ __global__ void __launch_bounds__(ln_block<GROUP>()) k_ln_bwd(const LnArgs a) {
       }
     }
   }
-  if (a.part) {
-    float* pw = a.part + group * 2 * a.cols;
-    float* pb = pw + a.cols;
+  griddep_launch_dependents();             // k_ln_finish
+  if (a.part) ln_write_part<VEC, GROUP, PER>(a, group, t, dw, db);
+}
+
+// ------------------------------------------------------ rows through a ring
+// Many rows of 16-byte aligned chunks: a block walks its rows, which arrive in
+// a ring in shared memory by bulk copies (one thread asks for a whole row),
+// several rows ahead.  Registers alone kept 16 to 32 KB per SM on their way
+// and reached 3 TB/s; the ring keeps about 100 KB.  A slot is refilled after
+// the block barrier of its row's first reduction, which every thread reaches
+// with the row in registers.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+constexpr int kLnMaxStages = 8;
+
+template <typename T, int GROUP, int PER>
+__global__ void __launch_bounds__(GROUP) k_ln_fwd_ring(const LnArgs a) {
+  constexpr int VEC = LnElem<T>::kVec;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 red[2][32];
+  __shared__ uint64_t full[kLnMaxStages];
+  __shared__ int abort_word;
+  const int t = threadIdx.x;
+  const uint32_t row_bytes = static_cast<uint32_t>(a.cols * sizeof(T));
+  const int64_t mine = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;   // rows of this block
+  if (t == 0) {
+    for (int i = 0; i < a.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  auto ask = [&](int64_t i, int s) {       // row i of this block into slot s
+    mbar_arrive_expect_tx(smem_u32(&full[s]), row_bytes);
+    bulk_load(smem_u32(ring) + s * row_bytes, static_cast<const T*>(a.x) + (blockIdx.x + i * gridDim.x) * a.ldx, row_bytes,
+              smem_u32(&full[s]));
+  };
+  if (t == 0)
+    for (int i = 0; i < a.stages && i < mine; ++i) ask(i, i);
+  float w[PER][VEC], b[PER][VEC];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
-      if (c < a.cols) {
-        if (VEC == 1) {
-          pw[c] = dw[i][0];
-          pb[c] = db[i][0];
-        } else {
+  for (int i = 0; i < PER; ++i) {
+    const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
+    if (c < a.cols) {
+      ln_param<VEC>(a.w, a.w_bf16, c, 1.0f, w[i]);
+      ln_param<VEC>(a.b, a.w_bf16, c, 0.0f, b[i]);
+    }
+  }
+  const float inv = 1.0f / static_cast<float>(a.cols);
+  int s = 0;
+  uint32_t parity = 0;
+  for (int64_t i = 0; i < mine; ++i) {
+    const int64_t row = blockIdx.x + i * gridDim.x;
+    // (a wait that gives up says so in *status; the rest of the launch runs out quickly)
+    mbar_wait(smem_u32(&full[s]), parity, &abort_word, a.status);
+    LnRaw<T, VEC> raw[PER];
+    float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int e = 0; e < VEC; e += 4) {
-            *reinterpret_cast<float4*>(pw + c + e) =
-                make_float4(dw[i][e], dw[i][(e + 1) % VEC], dw[i][(e + 2) % VEC], dw[i][(e + 3) % VEC]);
-            *reinterpret_cast<float4*>(pb + c + e) =
-                make_float4(db[i][e], db[i][(e + 1) % VEC], db[i][(e + 2) % VEC], db[i][(e + 3) % VEC]);
-          }
+    for (int k = 0; k < PER; ++k) {
+      const int64_t c = static_cast<int64_t>(t + k * GROUP) * VEC;
+      if (c < a.cols) raw[k].load(reinterpret_cast<const T*>(ring + s * row_bytes) + c); else raw[k].zero();
+      float f[VEC];
+      raw[k].get(f);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sum.x += f[e];
+    }
+    const float mean = ln_group_sum<GROUP>(sum, red[0]).x * inv;
+    if (t == 0 && i + a.stages < mine) ask(i + a.stages, s);
+    sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      float f[VEC];
+      raw[k].get(f);
+      if (static_cast<int64_t>(t + k * GROUP) * VEC < a.cols) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = f[e] - mean;
+          sum.x = fmaf(d, d, sum.x);
         }
       }
     }
+    const float rstd = 1.0f / sqrtf(ln_group_sum<GROUP>(sum, red[1]).x * inv + a.eps);
+    T* y = static_cast<T*>(a.y) + row * a.ldy;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int64_t c = static_cast<int64_t>(t + k * GROUP) * VEC;
+      if (c < a.cols) {
+        float f[VEC];
+        raw[k].get(f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[k][e], b[k][e]);
+        ln_store(y + c, f);
+      }
+    }
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    if (++s == a.stages) { s = 0; parity ^= 1; }
   }
+}
+
+template <typename T, int GROUP, int PER>
+__global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
+  constexpr int VEC = LnElem<T>::kVec;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 red[2][32];
+  __shared__ uint64_t full[kLnMaxStages];
+  __shared__ int abort_word;
+  const int t = threadIdx.x;
+  const uint32_t row_bytes = static_cast<uint32_t>(a.cols * sizeof(T));
+  const int64_t mine = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
+  if (t == 0) {
+    for (int i = 0; i < a.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  auto ask = [&](int64_t i, int s) {       // rows i of x and dy into slot s
+    const int64_t row = blockIdx.x + i * gridDim.x;
+    const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(ring) + 2 * s * row_bytes;
+    mbar_arrive_expect_tx(bar, 2 * row_bytes);
+    bulk_load(dst, static_cast<const T*>(a.x) + row * a.ldx, row_bytes, bar);
+    bulk_load(dst + row_bytes, static_cast<const T*>(a.dy) + row * a.lddy, row_bytes, bar);
+  };
+  if (t == 0)
+    for (int i = 0; i < a.stages && i < mine; ++i) ask(i, i);
+  float w[PER][VEC], dw[PER][VEC], db[PER][VEC];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) w[i][e] = dw[i][e] = db[i][e] = 0.0f;
+    if (c < a.cols) ln_param<VEC>(a.w, a.w_bf16, c, 1.0f, w[i]);
+  }
+  const float inv = 1.0f / static_cast<float>(a.cols);
+  int s = 0;
+  uint32_t parity = 0;
+  float mu = a.mean[blockIdx.x], rs = a.rstd[blockIdx.x];
+  for (int64_t i = 0; i < mine; ++i) {
+    const int64_t row = blockIdx.x + i * gridDim.x;
+    const int64_t next = i + 1 < mine ? row + gridDim.x : row;
+    const float mu_next = a.mean[next], rs_next = a.rstd[next];
+    mbar_wait(smem_u32(&full[s]), parity, &abort_word, a.status);
+    const T* xs = reinterpret_cast<const T*>(ring + 2 * s * row_bytes);
+    const T* ds = reinterpret_cast<const T*>(ring + (2 * s + 1) * row_bytes);
+    LnRaw<T, VEC> x[PER], d[PER];
+    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int64_t c = static_cast<int64_t>(t + k * GROUP) * VEC;
+      if (c < a.cols) { x[k].load(xs + c); d[k].load(ds + c); } else { x[k].zero(); d[k].zero(); }
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      // (past the last column w and dy are zero, so nothing is added)
+      float fx[VEC], fd[VEC];
+      x[k].get(fx);
+      d[k].get(fd);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float xh = (fx[e] - mu) * rs, g = fd[e] * w[k][e];
+        sum.x += g;
+        sum.y = fmaf(g, xh, sum.y);
+        dw[k][e] = fmaf(fd[e], xh, dw[k][e]);
+        db[k][e] += fd[e];
+      }
+    }
+    sum = ln_group_sum<GROUP>(sum, red[i & 1]);
+    if (t == 0 && i + a.stages < mine) ask(i + a.stages, s);
+    const float m1 = sum.x * inv, m2 = sum.y * inv;
+    T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int64_t c = static_cast<int64_t>(t + k * GROUP) * VEC;
+      if (c < a.cols) {
+        float fx[VEC], fd[VEC], o[VEC];
+        x[k].get(fx);
+        d[k].get(fd);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float xh = (fx[e] - mu) * rs;
+          o[e] = rs * (fmaf(fd[e], w[k][e], -m1) - xh * m2);
+        }
+        ln_store(dx + c, o);
+      }
+    }
+    mu = mu_next;
+    rs = rs_next;
+    if (++s == a.stages) { s = 0; parity ^= 1; }
+  }
+  griddep_launch_dependents();             // k_ln_finish
+  if (a.part) ln_write_part<VEC, GROUP, PER>(a, blockIdx.x, t, dw, db);
 }
 
 // Any row length: dx with a block per row, then the columns' partials with a
@@ -403,13 +604,16 @@ struct LnFinishArgs {
   void* dw;             // nullable
   void* db;             // nullable
   int out_bf16;
+  int dependent;        // launched behind the kernel that writes the partials
 };
 __global__ void __launch_bounds__(1024) k_ln_finish(const LnFinishArgs a) {
   __shared__ float2 sm[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + x;
   float2 s = make_float2(0.0f, 0.0f);
+  if (a.dependent) griddep_wait();
   if (c < a.cols) {
+#pragma unroll 4
     for (int p = y; p < a.parts; p += 32) {
       const float* q = a.part + static_cast<int64_t>(p) * 2 * a.cols + c;
       s.x += q[0];

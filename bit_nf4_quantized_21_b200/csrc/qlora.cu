@@ -1510,9 +1510,35 @@ LnPlan ln_plan(int64_t cols, int vec_elems, bool vec) {
   return {0, 0, false};
 }
 
+// Rows through the ring: when every resident block has a few rows to walk.
+// Fewer rows are a matter of latency, which setting the ring up only adds to.
+template <typename T, int GROUP, int PER, bool BWD>
+int ln_ring(LnArgs a, int max_parts, cudaStream_t cs) {
+  const int64_t slot = a.cols * static_cast<int64_t>(sizeof(T)) * (BWD ? 2 : 1);
+  const int per_sm = GROUP <= 256 ? 2 : GROUP <= 512 ? (BWD ? 1 : 2) : 1;
+  const int64_t budget = 200 * 1024 / per_sm;
+  a.stages = static_cast<int>(std::min<int64_t>(kLnMaxStages, budget / slot));
+  const int64_t blocks = static_cast<int64_t>(sm_count()) * per_sm;
+  if (a.stages < 2 || a.rows < 4 * blocks || (BWD && blocks > max_parts)) return 0;
+  const void* k = BWD ? reinterpret_cast<const void*>(k_ln_bwd_ring<T, GROUP, PER>)
+                      : reinterpret_cast<const void*>(k_ln_fwd_ring<T, GROUP, PER>);
+  const size_t smem = static_cast<size_t>(a.stages) * slot;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (BWD) k_ln_bwd_ring<T, GROUP, PER><<<static_cast<unsigned>(blocks), GROUP, smem, cs>>>(a);
+  else k_ln_fwd_ring<T, GROUP, PER><<<static_cast<unsigned>(blocks), GROUP, smem, cs>>>(a);
+  return static_cast<int>(blocks);
+}
+
 template <typename T, int VEC, int GROUP, int PER, bool BWD>
 int ln_launch(const LnArgs& a, int max_parts, cudaStream_t cs) {
   constexpr int kRows = ln_block<GROUP>() / GROUP;
+  if constexpr (VEC > 1 && GROUP >= 128 && (GROUP < 1024 || !BWD)) {   // (1024 threads: too few registers for dw, db)
+    const int parts = ln_ring<T, GROUP, PER, BWD>(a, max_parts, cs);
+    if (parts > 0) return parts;
+  }
   int64_t grid = cdiv(a.rows, kRows);
   if (!BWD) {
     k_ln_fwd<T, VEC, GROUP, PER><<<static_cast<unsigned>(grid), ln_block<GROUP>(), 0, cs>>>(a);
@@ -1574,7 +1600,7 @@ size_t qlora_layernorm_workspace_bytes(int64_t rows, int64_t cols) {
 
 qlora_status qlora_layernorm_fwd(const void* X, int64_t ldx, int64_t rows, int64_t cols, qlora_dtype dtype,
                                  const void* weight, const void* bias, qlora_dtype w_dtype, float eps, void* Y,
-                                 int64_t ldy, float* mean, float* rstd, void* stream) {
+                                 int64_t ldy, float* mean, float* rstd, int* d_status, void* stream) {
   NvtxRange nvtx_range("qlora_layernorm_fwd");
   if (!ln_shape(rows, cols) || ldx < cols || ldy < cols || !is_io_dtype(dtype) || !is_io_dtype(w_dtype))
     return QLORA_ERR_INVALID_ARG;
@@ -1587,6 +1613,7 @@ qlora_status qlora_layernorm_fwd(const void* X, int64_t ldx, int64_t rows, int64
   LnArgs a{};
   a.x = X; a.ldx = ldx; a.w = weight; a.b = bias; a.w_bf16 = w_dtype == QLORA_BF16 ? 1 : 0;
   a.rows = rows; a.cols = cols; a.eps = eps; a.y = Y; a.ldy = ldy; a.mean = mean; a.rstd = rstd;
+  a.status = d_status;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int v = dtype == QLORA_BF16 ? LnElem<__nv_bfloat16>::kVec : LnElem<float>::kVec;
   const bool vec = cols % v == 0 && rows16(X, ldx, es) && rows16(Y, ldy, es) && aligned16(weight) && aligned16(bias);
@@ -1605,7 +1632,7 @@ qlora_status qlora_layernorm_fwd(const void* X, int64_t ldx, int64_t rows, int64
 qlora_status qlora_layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx, int64_t rows, int64_t cols,
                                  qlora_dtype dtype, const void* weight, qlora_dtype w_dtype, const float* mean,
                                  const float* rstd, void* dX, int64_t lddx, void* dweight, void* dbias,
-                                 qlora_dtype grad_dtype, void* workspace, size_t ws_bytes, void* stream) {
+                                 qlora_dtype grad_dtype, void* workspace, size_t ws_bytes, int* d_status, void* stream) {
   NvtxRange nvtx_range("qlora_layernorm_bwd");
   if (!ln_shape(rows, cols) || ldx < cols || lddy < cols || lddx < cols || !is_io_dtype(dtype) ||
       !is_io_dtype(w_dtype) || !is_io_dtype(grad_dtype))
@@ -1628,7 +1655,7 @@ qlora_status qlora_layernorm_bwd(const void* dY, int64_t lddy, const void* X, in
     LnArgs a{};
     a.x = X; a.ldx = ldx; a.w = weight; a.w_bf16 = w_dtype == QLORA_BF16 ? 1 : 0;
     a.rows = rows; a.cols = cols; a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
-    a.dy = dY; a.lddy = lddy; a.dx = dX; a.lddx = lddx;
+    a.dy = dY; a.lddy = lddy; a.dx = dX; a.lddx = lddx; a.status = d_status;
     a.part = want ? static_cast<float*>(workspace) : nullptr;
     const int v = dtype == QLORA_BF16 ? LnElem<__nv_bfloat16>::kVec : LnElem<float>::kVec;
     const bool vec = cols % v == 0 && rows16(X, ldx, es) && rows16(dY, lddy, es) && rows16(dX, lddx, es) &&
@@ -1647,8 +1674,17 @@ qlora_status qlora_layernorm_bwd(const void* dY, int64_t lddy, const void* X, in
     LnFinishArgs f{};
     f.part = static_cast<const float*>(workspace);
     f.parts = parts; f.cols = cols; f.dw = dweight; f.db = dbias; f.out_bf16 = grad_dtype == QLORA_BF16 ? 1 : 0;
-    k_ln_finish<<<static_cast<unsigned>(cdiv(cols, 32)), 1024, 0, cs>>>(f);
-    return check_launch();
+    f.dependent = rows > 0 ? 1 : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cdiv(cols, 32)));
+    cfg.blockDim = dim3(1024);
+    cfg.stream = cs;
+    LaunchAttrs attrs(cfg, 1, rows > 0);
+    if (cudaLaunchKernelEx(&cfg, k_ln_finish, f) != cudaSuccess) {
+      cudaGetLastError();
+      return QLORA_ERR_CUDA;
+    }
+    return QLORA_OK;
   }
   return QLORA_OK;
 }

@@ -166,10 +166,10 @@ def lib() -> ctypes.CDLL:
                 f.restype = I32
             L.qlora_layernorm_workspace_bytes.argtypes = [I64, I64]
             L.qlora_layernorm_workspace_bytes.restype = ctypes.c_size_t
-            L.qlora_layernorm_fwd.argtypes = [P, I64, I64, I64, I32, P, P, I32, F, P, I64, P, P, P]
+            L.qlora_layernorm_fwd.argtypes = [P, I64, I64, I64, I32, P, P, I32, F, P, I64, P, P, P, P]
             L.qlora_layernorm_fwd.restype = I32
             L.qlora_layernorm_bwd.argtypes = [P, I64, P, I64, I64, I64, I32, P, I32, P, P, P, I64, P, P, I32, P,
-                                              ctypes.c_size_t, P]
+                                              ctypes.c_size_t, P, P]
             L.qlora_layernorm_bwd.restype = I32
             L.qlora_distill_topk_fwd.argtypes = [P, I64, I64, I64, I32, P, I32, P, I32, I32, F, P, P, P, P, I64, P, P]
             L.qlora_distill_topk_fwd.restype = I32
@@ -695,9 +695,9 @@ def _params(cols: int, *ps):
 
 def qlora_layernorm_fwd(X: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                         eps: float = 1e-5, Y: torch.Tensor | None = None, mean: torch.Tensor | None = None,
-                        rstd: torch.Tensor | None = None, stream=None):
+                        rstd: torch.Tensor | None = None, d_status: torch.Tensor | None = None, stream=None):
     """(Y, mean, rstd) of the rows of X [rows, cols]; mean and rstd (fp32 [rows]) are what the backward needs."""
-    with _on(stream, X, weight, bias, Y, mean, rstd):
+    with _on(stream, X, weight, bias, Y, mean, rstd, d_status):
         x, ldx = _matrix(X, "X")
         rows, cols = X.shape
         (w, b), wdt = _params(cols, weight, bias)
@@ -712,7 +712,7 @@ def qlora_layernorm_fwd(X: torch.Tensor, weight: torch.Tensor | None = None, bia
             rstd = torch.empty_like(mean)
         _check(lib().qlora_layernorm_fwd(x, ldx, rows, cols, _dtype(X, "X"), w, b, wdt, float(eps), y, ldy,
                                          _vector(mean, "mean", rows, torch.float32),
-                                         _vector(rstd, "rstd", rows, torch.float32), _current(X)),
+                                         _vector(rstd, "rstd", rows, torch.float32), _ptr(d_status), _current(X)),
                "qlora_layernorm_fwd")
     return Y, mean, rstd
 
@@ -720,9 +720,9 @@ def qlora_layernorm_fwd(X: torch.Tensor, weight: torch.Tensor | None = None, bia
 def qlora_layernorm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
                         rstd: torch.Tensor, dX: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
                         dbias: torch.Tensor | None = None, grad_dtype=torch.float32, want_params: bool = True,
-                        workspace: torch.Tensor | None = None, stream=None):
+                        workspace: torch.Tensor | None = None, d_status: torch.Tensor | None = None, stream=None):
     """(dX, dweight, dbias); want_params=False for a frozen norm (the two are None, unless given)."""
-    with _on(stream, dY, X, weight, mean, rstd, dX, dweight, dbias, workspace):
+    with _on(stream, dY, X, weight, mean, rstd, dX, dweight, dbias, workspace, d_status):
         x, ldx = _matrix(X, "X")
         rows, cols = X.shape
         dy, lddy = _matrix(dY, "dY", rows, cols)
@@ -753,7 +753,7 @@ def qlora_layernorm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor 
                                          _vector(mean, "mean", rows, torch.float32),
                                          _vector(rstd, "rstd", rows, torch.float32), dx, lddx,
                                          _vector(dweight, "dweight", cols), _vector(dbias, "dbias", cols), gdt, ws,
-                                         ws_bytes, _current(X)), "qlora_layernorm_bwd")
+                                         ws_bytes, _ptr(d_status), _current(X)), "qlora_layernorm_bwd")
     return dX, dweight, dbias
 
 

@@ -430,12 +430,12 @@ size_t qlora_layernorm_workspace_bytes(int64_t rows, int64_t cols);
 qlora_status qlora_layernorm_fwd(const void* X, int64_t ldx, int64_t rows, int64_t cols,
                                  qlora_dtype dtype, const void* weight, const void* bias,
                                  qlora_dtype w_dtype, float eps, void* Y, int64_t ldy, float* mean,
-                                 float* rstd, void* stream);
+                                 float* rstd, int* d_status, void* stream);
 qlora_status qlora_layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx,
                                  int64_t rows, int64_t cols, qlora_dtype dtype, const void* weight,
                                  qlora_dtype w_dtype, const float* mean, const float* rstd, void* dX,
                                  int64_t lddx, void* dweight, void* dbias, qlora_dtype grad_dtype,
-                                 void* workspace, size_t ws_bytes, void* stream);
+                                 void* workspace, size_t ws_bytes, int* d_status, void* stream);
 
 /*
  * Distillation from a teacher's top logits: the loss that a fine-tuning run

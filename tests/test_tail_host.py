@@ -87,7 +87,7 @@ def test_fp8_refuses_bad_calls():
 
 def test_layernorm_refusals():
     L = q.lib()
-    fwd = [FAKE, 64, 4, 64, 1, FAKE, FAKE, 1, 1e-5, FAKE, 64, FAKE, FAKE, None]
+    fwd = [FAKE, 64, 4, 64, 1, FAKE, FAKE, 1, 1e-5, FAKE, 64, FAKE, FAKE, None, None]
 
     def f(i, v):
         a = list(fwd)
@@ -99,7 +99,7 @@ def test_layernorm_refusals():
     need = q.qlora_layernorm_workspace_bytes(4, 64)
     assert need > 0 and q.qlora_layernorm_workspace_bytes(0, 64) == 0
     assert q.qlora_layernorm_workspace_bytes(-1, 64) == 0 and q.qlora_layernorm_workspace_bytes(4, 0) == 0
-    bwd = [FAKE, 64, FAKE, 64, 4, 64, 1, FAKE, 1, FAKE, FAKE, FAKE, 64, FAKE, FAKE, 0, FAKE, need, None]
+    bwd = [FAKE, 64, FAKE, 64, 4, 64, 1, FAKE, 1, FAKE, FAKE, FAKE, 64, FAKE, FAKE, 0, FAKE, need, None, None]
 
     def b(i, v):
         a = list(bwd)
