@@ -369,15 +369,75 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 constexpr int kLnMaxStages = 8;
 
-template <typename T, int GROUP, int PER>
-__global__ void __launch_bounds__(GROUP) k_ln_fwd_ring(const LnArgs a) {
-  constexpr int VEC = LnElem<T>::kVec;
+// Two fp32 values in one register pair (each operation rounds each value as
+// its scalar form does): the ring kernels' arithmetic per byte is what keeps
+// them from the memory's rate, and pairs halve its instructions.
+typedef uint64_t f32x2;
+__device__ __forceinline__ f32x2 pair2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// VEC elements from shared memory as pairs; zeros past the last column
+template <typename T, int VEC>
+__device__ __forceinline__ void ln_pairs(const T* p, bool in, f32x2 (&v)[VEC / 2]) {
+  LnRaw<T, VEC> raw;
+  if (in) raw.load(p); else raw.zero();
+  float f[VEC];
+  raw.get(f);
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) v[i] = pair2(f[2 * i], f[2 * i + 1]);
+}
+template <int VEC>
+__device__ __forceinline__ void ln_param_pairs(const void* p, int bf16, int64_t c, float fill, f32x2 (&v)[VEC / 2]) {
+  float f[VEC];
+  ln_param<VEC>(p, bf16, c, fill, f);
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) v[i] = pair2(f[2 * i], f[2 * i + 1]);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void ln_store_pairs(T* p, const f32x2 (&v)[VEC / 2]) {
+  float f[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) {
+    const float2 u = unpair2(v[i]);
+    f[2 * i] = u.x;
+    f[2 * i + 1] = u.y;
+  }
+  ln_store(p, f);
+}
+
+// FULL: the row is exactly GROUP * PER chunks, so no thread is past its end.
+template <typename T, int GROUP, int PER, bool FULL>
+__global__ void __launch_bounds__(GROUP, 1024 / GROUP) k_ln_fwd_ring(const LnArgs a) {
+  constexpr int VEC = LnElem<T>::kVec, H = VEC / 2;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][32];
   __shared__ uint64_t full[kLnMaxStages];
   __shared__ int abort_word;
   const int t = threadIdx.x;
-  const uint32_t row_bytes = static_cast<uint32_t>(a.cols * sizeof(T));
+  const int cols = static_cast<int>(a.cols);
+  const uint32_t row_bytes = static_cast<uint32_t>(cols * sizeof(T));
   const int64_t mine = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;   // rows of this block
   if (t == 0) {
     for (int i = 0; i < a.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
@@ -392,59 +452,57 @@ __global__ void __launch_bounds__(GROUP) k_ln_fwd_ring(const LnArgs a) {
   };
   if (t == 0)
     for (int i = 0; i < a.stages && i < mine; ++i) ask(i, i);
-  float w[PER][VEC], b[PER][VEC];
+  f32x2 w[PER][H], b[PER][H];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
-    if (c < a.cols) {
-      ln_param<VEC>(a.w, a.w_bf16, c, 1.0f, w[i]);
-      ln_param<VEC>(a.b, a.w_bf16, c, 0.0f, b[i]);
+  for (int k = 0; k < PER; ++k) {
+    const int c = (t + k * GROUP) * VEC;
+    if (FULL || c < cols) {
+      ln_param_pairs<VEC>(a.w, a.w_bf16, c, 1.0f, w[k]);
+      ln_param_pairs<VEC>(a.b, a.w_bf16, c, 0.0f, b[k]);
     }
   }
-  const float inv = 1.0f / static_cast<float>(a.cols);
+  const float inv = 1.0f / static_cast<float>(cols);
   int s = 0;
   uint32_t parity = 0;
   for (int64_t i = 0; i < mine; ++i) {
     const int64_t row = blockIdx.x + i * gridDim.x;
     // (a wait that gives up says so in *status; the rest of the launch runs out quickly)
     mbar_wait(smem_u32(&full[s]), parity, &abort_word, a.status);
-    LnRaw<T, VEC> raw[PER];
-    float2 sum = make_float2(0.0f, 0.0f);
+    const T* src = reinterpret_cast<const T*>(ring + s * row_bytes);
+    f32x2 v[PER][H], acc = 0;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int64_t c = static_cast<int64_t>(t + k * GROUP) * VEC;
-      if (c < a.cols) raw[k].load(reinterpret_cast<const T*>(ring + s * row_bytes) + c); else raw[k].zero();
-      float f[VEC];
-      raw[k].get(f);
+      const int c = (t + k * GROUP) * VEC;
+      ln_pairs<T, VEC>(src + c, FULL || c < cols, v[k]);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) sum.x += f[e];
+      for (int e = 0; e < H; ++e) acc = add2(acc, v[k][e]);
     }
-    const float mean = ln_group_sum<GROUP>(sum, red[0]).x * inv;
+    float2 sum = unpair2(acc);
+    const float mean = ln_group_sum<GROUP>(make_float2(sum.x + sum.y, 0.0f), red[0]).x * inv;
     if (t == 0 && i + a.stages < mine) ask(i + a.stages, s);
-    sum = make_float2(0.0f, 0.0f);
+    const f32x2 neg = pair2(-mean, -mean);
+    acc = 0;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      float f[VEC];
-      raw[k].get(f);
-      if (static_cast<int64_t>(t + k * GROUP) * VEC < a.cols) {
+      if (FULL || (t + k * GROUP) * VEC < cols) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float d = f[e] - mean;
-          sum.x = fmaf(d, d, sum.x);
+        for (int e = 0; e < H; ++e) {
+          v[k][e] = add2(v[k][e], neg);
+          acc = fma2(v[k][e], v[k][e], acc);
         }
       }
     }
-    const float rstd = 1.0f / sqrtf(ln_group_sum<GROUP>(sum, red[1]).x * inv + a.eps);
+    sum = unpair2(acc);
+    const float rstd = 1.0f / sqrtf(ln_group_sum<GROUP>(make_float2(sum.x + sum.y, 0.0f), red[1]).x * inv + a.eps);
+    const f32x2 scale = pair2(rstd, rstd);
     T* y = static_cast<T*>(a.y) + row * a.ldy;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int64_t c = static_cast<int64_t>(t + k * GROUP) * VEC;
-      if (c < a.cols) {
-        float f[VEC];
-        raw[k].get(f);
+      const int c = (t + k * GROUP) * VEC;
+      if (FULL || c < cols) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[k][e], b[k][e]);
-        ln_store(y + c, f);
+        for (int e = 0; e < H; ++e) v[k][e] = fma2(mul2(v[k][e], scale), w[k][e], b[k][e]);
+        ln_store_pairs<T, VEC>(y + c, v[k]);
       }
     }
     if (t == 0) {
@@ -455,15 +513,16 @@ __global__ void __launch_bounds__(GROUP) k_ln_fwd_ring(const LnArgs a) {
   }
 }
 
-template <typename T, int GROUP, int PER>
+template <typename T, int GROUP, int PER, bool FULL>
 __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
-  constexpr int VEC = LnElem<T>::kVec;
+  constexpr int VEC = LnElem<T>::kVec, H = VEC / 2;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][32];
   __shared__ uint64_t full[kLnMaxStages];
   __shared__ int abort_word;
   const int t = threadIdx.x;
-  const uint32_t row_bytes = static_cast<uint32_t>(a.cols * sizeof(T));
+  const int cols = static_cast<int>(a.cols);
+  const uint32_t row_bytes = static_cast<uint32_t>(cols * sizeof(T));
   const int64_t mine = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
   if (t == 0) {
     for (int i = 0; i < a.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
@@ -480,15 +539,15 @@ __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
   };
   if (t == 0)
     for (int i = 0; i < a.stages && i < mine; ++i) ask(i, i);
-  float w[PER][VEC], dw[PER][VEC], db[PER][VEC];
+  f32x2 w[PER][H], dw[PER][H], db[PER][H];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
+  for (int k = 0; k < PER; ++k) {
+    const int c = (t + k * GROUP) * VEC;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) w[i][e] = dw[i][e] = db[i][e] = 0.0f;
-    if (c < a.cols) ln_param<VEC>(a.w, a.w_bf16, c, 1.0f, w[i]);
+    for (int e = 0; e < H; ++e) w[k][e] = dw[k][e] = db[k][e] = 0;
+    if (FULL || c < cols) ln_param_pairs<VEC>(a.w, a.w_bf16, c, 1.0f, w[k]);
   }
-  const float inv = 1.0f / static_cast<float>(a.cols);
+  const float inv = 1.0f / static_cast<float>(cols);
   int s = 0;
   uint32_t parity = 0;
   float mu = a.mean[blockIdx.x], rs = a.rstd[blockIdx.x];
@@ -499,45 +558,37 @@ __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
     mbar_wait(smem_u32(&full[s]), parity, &abort_word, a.status);
     const T* xs = reinterpret_cast<const T*>(ring + 2 * s * row_bytes);
     const T* ds = reinterpret_cast<const T*>(ring + (2 * s + 1) * row_bytes);
-    LnRaw<T, VEC> x[PER], d[PER];
-    float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int64_t c = static_cast<int64_t>(t + k * GROUP) * VEC;
-      if (c < a.cols) { x[k].load(xs + c); d[k].load(ds + c); } else { x[k].zero(); d[k].zero(); }
-    }
+    const f32x2 neg = pair2(-mu, -mu), scale = pair2(rs, rs);
+    f32x2 xh[PER][H], g[PER][H], sg = 0, sgx = 0;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       // (past the last column w and dy are zero, so nothing is added)
-      float fx[VEC], fd[VEC];
-      x[k].get(fx);
-      d[k].get(fd);
+      const int c = (t + k * GROUP) * VEC;
+      ln_pairs<T, VEC>(xs + c, FULL || c < cols, xh[k]);
+      ln_pairs<T, VEC>(ds + c, FULL || c < cols, g[k]);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float xh = (fx[e] - mu) * rs, g = fd[e] * w[k][e];
-        sum.x += g;
-        sum.y = fmaf(g, xh, sum.y);
-        dw[k][e] = fmaf(fd[e], xh, dw[k][e]);
-        db[k][e] += fd[e];
+      for (int e = 0; e < H; ++e) {
+        xh[k][e] = mul2(add2(xh[k][e], neg), scale);
+        dw[k][e] = fma2(g[k][e], xh[k][e], dw[k][e]);
+        db[k][e] = add2(db[k][e], g[k][e]);
+        g[k][e] = mul2(g[k][e], w[k][e]);
+        sg = add2(sg, g[k][e]);
+        sgx = fma2(g[k][e], xh[k][e], sgx);
       }
     }
-    sum = ln_group_sum<GROUP>(sum, red[i & 1]);
+    const float2 p = unpair2(sg), q = unpair2(sgx);
+    const float2 sum = ln_group_sum<GROUP>(make_float2(p.x + p.y, q.x + q.y), red[i & 1]);
     if (t == 0 && i + a.stages < mine) ask(i + a.stages, s);
-    const float m1 = sum.x * inv, m2 = sum.y * inv;
+    const float m1 = -sum.x * inv, m2 = -sum.y * inv;
+    const f32x2 n1 = pair2(m1, m1), n2 = pair2(m2, m2);
     T* dx = static_cast<T*>(a.dx) + row * a.lddx;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int64_t c = static_cast<int64_t>(t + k * GROUP) * VEC;
-      if (c < a.cols) {
-        float fx[VEC], fd[VEC], o[VEC];
-        x[k].get(fx);
-        d[k].get(fd);
+      const int c = (t + k * GROUP) * VEC;
+      if (FULL || c < cols) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float xh = (fx[e] - mu) * rs;
-          o[e] = rs * (fmaf(fd[e], w[k][e], -m1) - xh * m2);
-        }
-        ln_store(dx + c, o);
+        for (int e = 0; e < H; ++e) g[k][e] = mul2(fma2(xh[k][e], n2, add2(g[k][e], n1)), scale);
+        ln_store_pairs<T, VEC>(dx + c, g[k]);
       }
     }
     mu = mu_next;
@@ -545,7 +596,18 @@ __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
     if (++s == a.stages) { s = 0; parity ^= 1; }
   }
   griddep_launch_dependents();             // k_ln_finish
-  if (a.part) ln_write_part<VEC, GROUP, PER>(a, blockIdx.x, t, dw, db);
+  if (a.part) {
+    float fw[PER][VEC], fb[PER][VEC];
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+#pragma unroll
+      for (int e = 0; e < H; ++e) {
+        const float2 u = unpair2(dw[k][e]), v = unpair2(db[k][e]);
+        fw[k][2 * e] = u.x; fw[k][2 * e + 1] = u.y;
+        fb[k][2 * e] = v.x; fb[k][2 * e + 1] = v.y;
+      }
+    ln_write_part<VEC, GROUP, PER>(a, blockIdx.x, t, fw, fb);
+  }
 }
 
 // Any row length: dx with a block per row, then the columns' partials with a

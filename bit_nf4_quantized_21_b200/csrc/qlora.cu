@@ -1515,20 +1515,21 @@ LnPlan ln_plan(int64_t cols, int vec_elems, bool vec) {
 template <typename T, int GROUP, int PER, bool BWD>
 int ln_ring(LnArgs a, int max_parts, cudaStream_t cs) {
   const int64_t slot = a.cols * static_cast<int64_t>(sizeof(T)) * (BWD ? 2 : 1);
-  const int per_sm = GROUP <= 256 ? 2 : GROUP <= 512 ? (BWD ? 1 : 2) : 1;
+  const int per_sm = BWD ? (GROUP <= 256 ? 512 / GROUP : 1) : 1024 / GROUP;
   const int64_t budget = 200 * 1024 / per_sm;
   a.stages = static_cast<int>(std::min<int64_t>(kLnMaxStages, budget / slot));
   const int64_t blocks = static_cast<int64_t>(sm_count()) * per_sm;
   if (a.stages < 2 || a.rows < 4 * blocks || (BWD && blocks > max_parts)) return 0;
-  const void* k = BWD ? reinterpret_cast<const void*>(k_ln_bwd_ring<T, GROUP, PER>)
-                      : reinterpret_cast<const void*>(k_ln_fwd_ring<T, GROUP, PER>);
+  const bool full = a.cols == static_cast<int64_t>(GROUP) * PER * LnElem<T>::kVec;
+  void (*k)(LnArgs);
+  if constexpr (BWD) k = full ? k_ln_bwd_ring<T, GROUP, PER, true> : k_ln_bwd_ring<T, GROUP, PER, false>;
+  else k = full ? k_ln_fwd_ring<T, GROUP, PER, true> : k_ln_fwd_ring<T, GROUP, PER, false>;
   const size_t smem = static_cast<size_t>(a.stages) * slot;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
-  if (BWD) k_ln_bwd_ring<T, GROUP, PER><<<static_cast<unsigned>(blocks), GROUP, smem, cs>>>(a);
-  else k_ln_fwd_ring<T, GROUP, PER><<<static_cast<unsigned>(blocks), GROUP, smem, cs>>>(a);
+  k<<<static_cast<unsigned>(blocks), GROUP, smem, cs>>>(a);
   return static_cast<int>(blocks);
 }
 
