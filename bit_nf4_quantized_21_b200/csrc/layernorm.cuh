@@ -147,10 +147,27 @@ __device__ __forceinline__ float2 ln_group_sum(float2 v, float2* red) {
   __syncthreads();
   float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < GROUP / 32; ++i) {
-    const float2 u = red[i];
-    s.x += u.x;
-    s.y += u.y;
+  for (int i = 0; i < GROUP / 64; ++i) {
+    const float4 u = reinterpret_cast<const float4*>(red)[i];   // two warps' sums
+    s.x += u.x + u.z;
+    s.y += u.y + u.w;
+  }
+  return s;
+}
+// the same for one value; `red` as one float per warp
+template <int GROUP>
+__device__ __forceinline__ float ln_group_sum1(float v, float2* red2) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if (GROUP == 32) return v;
+  float* red = reinterpret_cast<float*>(red2);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < GROUP / 128; ++i) {
+    const float4 u = reinterpret_cast<const float4*>(red)[i];   // four warps' sums
+    s += (u.x + u.y) + (u.z + u.w);
   }
   return s;
 }
@@ -160,13 +177,13 @@ template <int GROUP> constexpr int ln_block() { return GROUP < 128 ? 128 : GROUP
 template <typename T, int VEC, int GROUP, int PER>
 __global__ void __launch_bounds__(ln_block<GROUP>()) k_ln_fwd(const LnArgs a) {
   constexpr int kRows = ln_block<GROUP>() / GROUP;
-  __shared__ float2 red[2][32];
+  __shared__ __align__(16) float2 red[2][32];
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / GROUP;
   const int t = threadIdx.x % GROUP;
   if (row >= a.rows) return;            // whole warps only: a group of a warp, or the block's one row
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   LnRaw<T, VEC> raw[PER];
-  float2 s = make_float2(0.0f, 0.0f);
+  float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
@@ -177,11 +194,11 @@ __global__ void __launch_bounds__(ln_block<GROUP>()) k_ln_fwd(const LnArgs a) {
     float f[VEC];
     raw[i].get(f);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) s.x += f[e];
+    for (int e = 0; e < VEC; ++e) s += f[e];
   }
   const float inv = 1.0f / static_cast<float>(a.cols);
-  const float mean = ln_group_sum<GROUP>(s, red[0]).x * inv;
-  s = make_float2(0.0f, 0.0f);
+  const float mean = ln_group_sum1<GROUP>(s, red[0]) * inv;
+  s = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int64_t c = static_cast<int64_t>(t + i * GROUP) * VEC;
@@ -191,11 +208,11 @@ __global__ void __launch_bounds__(ln_block<GROUP>()) k_ln_fwd(const LnArgs a) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float d = f[e] - mean;
-        s.x = fmaf(d, d, s.x);
+        s = fmaf(d, d, s);
       }
     }
   }
-  const float rstd = 1.0f / sqrtf(ln_group_sum<GROUP>(s, red[1]).x * inv + a.eps);
+  const float rstd = 1.0f / sqrtf(ln_group_sum1<GROUP>(s, red[1]) * inv + a.eps);
   T* y = static_cast<T*>(a.y) + row * a.ldy;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -220,19 +237,19 @@ __global__ void __launch_bounds__(ln_block<GROUP>()) k_ln_fwd(const LnArgs a) {
 constexpr int kLnStreamThreads = 512;
 template <typename T>
 __global__ void __launch_bounds__(kLnStreamThreads) k_ln_fwd_stream(const LnArgs a) {
-  __shared__ float2 red[2][32];
+  __shared__ __align__(16) float2 red[2][32];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const float inv = 1.0f / static_cast<float>(a.cols);
-  float2 s = make_float2(0.0f, 0.0f);
-  for (int64_t c = threadIdx.x; c < a.cols; c += kLnStreamThreads) s.x += static_cast<float>(x[c]);
-  const float mean = ln_group_sum<kLnStreamThreads>(s, red[0]).x * inv;
-  s.x = 0.0f;
+  float s = 0.0f;
+  for (int64_t c = threadIdx.x; c < a.cols; c += kLnStreamThreads) s += static_cast<float>(x[c]);
+  const float mean = ln_group_sum1<kLnStreamThreads>(s, red[0]) * inv;
+  s = 0.0f;
   for (int64_t c = threadIdx.x; c < a.cols; c += kLnStreamThreads) {
     const float d = static_cast<float>(x[c]) - mean;
-    s.x = fmaf(d, d, s.x);
+    s = fmaf(d, d, s);
   }
-  const float rstd = 1.0f / sqrtf(ln_group_sum<kLnStreamThreads>(s, red[1]).x * inv + a.eps);
+  const float rstd = 1.0f / sqrtf(ln_group_sum1<kLnStreamThreads>(s, red[1]) * inv + a.eps);
   T* y = static_cast<T*>(a.y) + row * a.ldy;
   for (int64_t c = threadIdx.x; c < a.cols; c += kLnStreamThreads) {
     float w[1], b[1], f[1];
@@ -278,7 +295,7 @@ __device__ __forceinline__ void ln_write_part(const LnArgs& a, int64_t group, in
 template <typename T, int VEC, int GROUP, int PER>
 __global__ void __launch_bounds__(ln_block<GROUP>()) k_ln_bwd(const LnArgs a) {
   constexpr int kRows = ln_block<GROUP>() / GROUP;
-  __shared__ float2 red[2][32];
+  __shared__ __align__(16) float2 red[2][32];
   const int t = threadIdx.x % GROUP;
   const int64_t group = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / GROUP;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
@@ -432,7 +449,7 @@ template <typename T, int GROUP, int PER, bool FULL>
 __global__ void __launch_bounds__(GROUP, 1024 / GROUP) k_ln_fwd_ring(const LnArgs a) {
   constexpr int VEC = LnElem<T>::kVec, H = VEC / 2;
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 red[2][32];
+  __shared__ __align__(16) float2 red[2][32];
   __shared__ uint64_t full[kLnMaxStages];
   __shared__ int abort_word;
   const int t = threadIdx.x;
@@ -478,7 +495,7 @@ __global__ void __launch_bounds__(GROUP, 1024 / GROUP) k_ln_fwd_ring(const LnArg
       for (int e = 0; e < H; ++e) acc = add2(acc, v[k][e]);
     }
     float2 sum = unpair2(acc);
-    const float mean = ln_group_sum<GROUP>(make_float2(sum.x + sum.y, 0.0f), red[0]).x * inv;
+    const float mean = ln_group_sum1<GROUP>(sum.x + sum.y, red[0]) * inv;
     if (t == 0 && i + a.stages < mine) ask(i + a.stages, s);
     const f32x2 neg = pair2(-mean, -mean);
     acc = 0;
@@ -493,7 +510,7 @@ __global__ void __launch_bounds__(GROUP, 1024 / GROUP) k_ln_fwd_ring(const LnArg
       }
     }
     sum = unpair2(acc);
-    const float rstd = 1.0f / sqrtf(ln_group_sum<GROUP>(make_float2(sum.x + sum.y, 0.0f), red[1]).x * inv + a.eps);
+    const float rstd = 1.0f / sqrtf(ln_group_sum1<GROUP>(sum.x + sum.y, red[1]) * inv + a.eps);
     const f32x2 scale = pair2(rstd, rstd);
     T* y = static_cast<T*>(a.y) + row * a.ldy;
 #pragma unroll
@@ -517,7 +534,7 @@ template <typename T, int GROUP, int PER, bool FULL>
 __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
   constexpr int VEC = LnElem<T>::kVec, H = VEC / 2;
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 red[2][32];
+  __shared__ __align__(16) float2 red[2][32];
   __shared__ uint64_t full[kLnMaxStages];
   __shared__ int abort_word;
   const int t = threadIdx.x;
@@ -614,7 +631,7 @@ __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
 // thread per column and a run of rows per block row of the grid.
 template <typename T>
 __global__ void __launch_bounds__(kLnStreamThreads) k_ln_bwd_stream(const LnArgs a) {
-  __shared__ float2 red[2][32];
+  __shared__ __align__(16) float2 red[2][32];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
