@@ -22,7 +22,7 @@
 //
 // The backward walks rows with a fixed grid: a thread keeps the same columns
 // for every row, so its share of dw and db accumulates in registers and is
-// written once per group as a row of partials; k_ln_finish adds the partials
+// written once per block as a row of partials; k_ln_finish adds the partials
 // in a fixed order (no atomics: results do not depend on scheduling).
 #pragma once
 #include <cuda_bf16.h>
@@ -173,6 +173,8 @@ __device__ __forceinline__ float ln_group_sum1(float v, float2* red2) {
 }
 
 template <int GROUP> constexpr int ln_block() { return GROUP < 128 ? 128 : GROUP; }
+// backward: eight warps' rows, whose partials the block adds up itself
+template <int GROUP> constexpr int ln_bwd_block() { return GROUP < 128 ? 256 : GROUP; }
 
 template <typename T, int VEC, int GROUP, int PER>
 __global__ void __launch_bounds__(ln_block<GROUP>()) k_ln_fwd(const LnArgs a) {
@@ -293,8 +295,8 @@ __device__ __forceinline__ void ln_write_part(const LnArgs& a, int64_t group, in
 // Backward, rows in registers.  The grid walks the rows; the loads of the
 // next row are in flight while the current one is reduced.
 template <typename T, int VEC, int GROUP, int PER>
-__global__ void __launch_bounds__(ln_block<GROUP>()) k_ln_bwd(const LnArgs a) {
-  constexpr int kRows = ln_block<GROUP>() / GROUP;
+__global__ void __launch_bounds__(ln_bwd_block<GROUP>(), GROUP <= 512 ? 2 : 1) k_ln_bwd(const LnArgs a) {
+  constexpr int kRows = ln_bwd_block<GROUP>() / GROUP;
   __shared__ __align__(16) float2 red[2][32];
   const int t = threadIdx.x % GROUP;
   const int64_t group = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / GROUP;
@@ -369,7 +371,30 @@ __global__ void __launch_bounds__(ln_block<GROUP>()) k_ln_bwd(const LnArgs a) {
     }
   }
   griddep_launch_dependents();             // k_ln_finish
-  if (a.part) ln_write_part<VEC, GROUP, PER>(a, group, t, dw, db);
+  if (!a.part) return;
+  if (kRows == 1) {
+    ln_write_part<VEC, GROUP, PER>(a, group, t, dw, db);
+  } else {
+    // one row of partials per block: the warps' sums added in warp order
+    constexpr int kCols = GROUP * PER * VEC;
+    __shared__ float sums[kRows][kRows == 1 ? 1 : kCols];
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sums[threadIdx.x / GROUP][(t + i * GROUP) * VEC + e] = which ? db[i][e] : dw[i][e];
+      __syncthreads();
+      float* p = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + which) * a.cols;
+      for (int c = threadIdx.x; c < a.cols; c += ln_bwd_block<GROUP>()) {
+        float v = sums[0][c];
+#pragma unroll
+        for (int k = 1; k < kRows; ++k) v += sums[k][c];
+        p[c] = v;
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------ rows through a ring
@@ -674,8 +699,9 @@ __global__ void __launch_bounds__(kLnColThreads) k_ln_bwd_cols(const LnArgs a) {
   pw[a.cols + c] = db;
 }
 
-// dw and db from the partial rows: 32 columns per block, 32 row lanes, the
-// lanes' sums added in a fixed tree.
+// dw and db from the partial rows, which are read as rows of 2 cols values:
+// 32 of them per block, 16 bytes per thread, 32 threads down the rows with
+// all their loads in flight; the threads' sums are added in a fixed order.
 struct LnFinishArgs {
   const float* part;
   int parts;
@@ -685,38 +711,45 @@ struct LnFinishArgs {
   int out_bf16;
   int dependent;        // launched behind the kernel that writes the partials
 };
-__global__ void __launch_bounds__(1024) k_ln_finish(const LnFinishArgs a) {
-  __shared__ float2 sm[32][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + x;
-  float2 s = make_float2(0.0f, 0.0f);
+constexpr int kLnFinishThreads = 256;
+constexpr int kLnFinishCols = 32, kLnFinishLanes = kLnFinishThreads * 4 / kLnFinishCols;
+constexpr int kLnFinishLoads = (kLnMaxParts + kLnFinishLanes - 1) / kLnFinishLanes;
+__global__ void __launch_bounds__(kLnFinishThreads) k_ln_finish(const LnFinishArgs a) {
+  __shared__ float sm[kLnFinishLanes][kLnFinishCols + 1];
+  const int x = (threadIdx.x % 8) * 4, y = threadIdx.x / 8;
+  const int64_t width = 2 * a.cols, c0 = static_cast<int64_t>(blockIdx.x) * kLnFinishCols + x;
   if (a.dependent) griddep_wait();
-  if (c < a.cols) {
-#pragma unroll 4
-    for (int p = y; p < a.parts; p += 32) {
-      const float* q = a.part + static_cast<int64_t>(p) * 2 * a.cols + c;
-      s.x += q[0];
-      s.y += q[a.cols];
-    }
-  }
-  sm[y][x] = s;
-  __syncthreads();
-  // row y of the transposed tile: column y's 32 lane sums in one warp
-  s = sm[x][y];
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (c0 + 4 <= width && width % 4 == 0) {
+    float4 v[kLnFinishLoads];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, o);
-    s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, o);
-  }
-  const int64_t oc = static_cast<int64_t>(blockIdx.x) * 32 + y;
-  if (x == 0 && oc < a.cols) {
-    if (a.out_bf16) {
-      if (a.dw) static_cast<__nv_bfloat16*>(a.dw)[oc] = __float2bfloat16_rn(s.x);
-      if (a.db) static_cast<__nv_bfloat16*>(a.db)[oc] = __float2bfloat16_rn(s.y);
-    } else {
-      if (a.dw) static_cast<float*>(a.dw)[oc] = s.x;
-      if (a.db) static_cast<float*>(a.db)[oc] = s.y;
+    for (int i = 0; i < kLnFinishLoads; ++i) {
+      const int p = y + i * kLnFinishLanes;
+      v[i] = p < a.parts ? *reinterpret_cast<const float4*>(a.part + p * width + c0) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
+#pragma unroll
+    for (int i = 0; i < kLnFinishLoads; ++i) { s.x += v[i].x; s.y += v[i].y; s.z += v[i].z; s.w += v[i].w; }
+  } else {
+    for (int p = y; p < a.parts; p += kLnFinishLanes) {
+      const float* q = a.part + p * width + c0;
+      if (c0 < width) s.x += q[0];
+      if (c0 + 1 < width) s.y += q[1];
+      if (c0 + 2 < width) s.z += q[2];
+      if (c0 + 3 < width) s.w += q[3];
+    }
+  }
+  sm[y][x] = s.x; sm[y][x + 1] = s.y; sm[y][x + 2] = s.z; sm[y][x + 3] = s.w;
+  __syncthreads();
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kLnFinishCols + threadIdx.x;
+  if (threadIdx.x < kLnFinishCols && c < width) {
+    float v = sm[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < kLnFinishLanes; ++i) v += sm[i][threadIdx.x];
+    void* out = c < a.cols ? a.dw : a.db;
+    const int64_t at = c < a.cols ? c : c - a.cols;
+    if (!out) return;
+    if (a.out_bf16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+    else static_cast<float*>(out)[at] = v;
   }
 }
 

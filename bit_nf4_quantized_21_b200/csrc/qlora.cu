@@ -1536,6 +1536,13 @@ int ln_ring(LnArgs a, int max_parts, cudaStream_t cs) {
 template <typename T, int VEC, int GROUP, int PER, bool BWD>
 int ln_launch(const LnArgs& a, int max_parts, cudaStream_t cs) {
   constexpr int kRows = ln_block<GROUP>() / GROUP;
+  if constexpr (VEC > 1 && GROUP == 32 && PER == 4 && BWD) {
+    // a warp per row is short of registers here: 128 threads per row where the ring pays
+    if (a.cols > 64 * VEC) {
+      const int parts = ln_ring<T, 128, 1, true>(a, max_parts, cs);
+      if (parts > 0) return parts;
+    }
+  }
   if constexpr (VEC > 1 && GROUP >= 128 && (GROUP < 1024 || !BWD)) {   // (1024 threads: too few registers for dw, db)
     const int parts = ln_ring<T, GROUP, PER, BWD>(a, max_parts, cs);
     if (parts > 0) return parts;
@@ -1545,11 +1552,13 @@ int ln_launch(const LnArgs& a, int max_parts, cudaStream_t cs) {
     k_ln_fwd<T, VEC, GROUP, PER><<<static_cast<unsigned>(grid), ln_block<GROUP>(), 0, cs>>>(a);
     return 0;
   }
-  // one wave of resident blocks
-  const int per_sm = std::max(1, 1024 / ln_block<GROUP>() / 2);
-  grid = std::min<int64_t>(grid, std::min<int64_t>(static_cast<int64_t>(sm_count()) * per_sm, max_parts / kRows));
-  k_ln_bwd<T, VEC, GROUP, PER><<<static_cast<unsigned>(grid), ln_block<GROUP>(), 0, cs>>>(a);
-  return static_cast<int>(grid * kRows);
+  // one wave of resident blocks, each of which writes a row of partials
+  constexpr int kBlock = ln_bwd_block<GROUP>();
+  constexpr int per_sm = GROUP < 128 ? 3 : GROUP <= 512 ? 1024 / GROUP : 1;
+  grid = std::min<int64_t>(cdiv(a.rows, kBlock / GROUP),
+                           std::min<int64_t>(static_cast<int64_t>(sm_count()) * std::min(per_sm, 4), max_parts));
+  k_ln_bwd<T, VEC, GROUP, PER><<<static_cast<unsigned>(grid), kBlock, 0, cs>>>(a);
+  return static_cast<int>(grid);
 }
 
 // Launches the row kernel of a plan; returns the partial rows written.
@@ -1559,7 +1568,7 @@ int ln_rows(const LnArgs& a, const LnPlan& p, int max_parts, cudaStream_t cs) {
   if (p.vec) {
     if (p.group == 32 && p.per == 1) return ln_launch<T, V, 32, 1, BWD>(a, max_parts, cs);
     if (p.group == 32 && p.per == 2) return ln_launch<T, V, 32, 2, BWD>(a, max_parts, cs);
-    if (p.group == 32) return ln_launch<T, V, 32, 4, BWD>(a, max_parts, cs);
+    if (p.group == 32 && p.per == 4) return ln_launch<T, V, 32, 4, BWD>(a, max_parts, cs);
     if (p.group == 128) return ln_launch<T, V, 128, 2, BWD>(a, max_parts, cs);
     if (p.group == 256) return ln_launch<T, V, 256, 2, BWD>(a, max_parts, cs);
     if (p.group == 512) return ln_launch<T, V, 512, 2, BWD>(a, max_parts, cs);
@@ -1595,8 +1604,7 @@ extern "C" {
 
 size_t qlora_layernorm_workspace_bytes(int64_t rows, int64_t cols) {
   if (!ln_shape(rows, cols)) return 0;
-  // a group of a warp has company in its block: whole blocks write partials
-  return static_cast<size_t>(std::min<int64_t>(rup(rows, 4), kLnMaxParts)) * 2 * cols * 4;
+  return static_cast<size_t>(std::min<int64_t>(rows, kLnMaxParts)) * 2 * cols * 4;
 }
 
 qlora_status qlora_layernorm_fwd(const void* X, int64_t ldx, int64_t rows, int64_t cols, qlora_dtype dtype,
@@ -1662,7 +1670,7 @@ qlora_status qlora_layernorm_bwd(const void* dY, int64_t lddy, const void* X, in
     const bool vec = cols % v == 0 && rows16(X, ldx, es) && rows16(dY, lddy, es) && rows16(dX, lddx, es) &&
                      aligned16(weight);
     const LnPlan p = ln_plan(cols, v, vec);
-    const int max_parts = static_cast<int>(std::min<int64_t>(rup(rows, 4), kLnMaxParts));
+    const int max_parts = static_cast<int>(std::min<int64_t>(rows, kLnMaxParts));
     if (p.group == 0)
       parts = dtype == QLORA_BF16 ? ln_bwd_stream<__nv_bfloat16>(a, max_parts, cs) : ln_bwd_stream<float>(a, max_parts, cs);
     else
@@ -1677,8 +1685,8 @@ qlora_status qlora_layernorm_bwd(const void* dY, int64_t lddy, const void* X, in
     f.parts = parts; f.cols = cols; f.dw = dweight; f.db = dbias; f.out_bf16 = grad_dtype == QLORA_BF16 ? 1 : 0;
     f.dependent = rows > 0 ? 1 : 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cdiv(cols, 32)));
-    cfg.blockDim = dim3(1024);
+    cfg.gridDim = dim3(static_cast<unsigned>(cdiv(2 * cols, kLnFinishCols)));
+    cfg.blockDim = dim3(kLnFinishThreads);
     cfg.stream = cs;
     LaunchAttrs attrs(cfg, 1, rows > 0);
     if (cudaLaunchKernelEx(&cfg, k_ln_finish, f) != cudaSuccess) {
