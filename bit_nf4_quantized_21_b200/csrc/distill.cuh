@@ -25,19 +25,23 @@
 // vocabulary: one CTA when there are rows enough to fill the GPU, up to
 // eight for few rows; the CTAs exchange (m, s) through distributed shared
 // memory and combine them in rank order, so the result does not depend on
-// scheduling.  Rows may start at any element: the vector part of a row runs
+// scheduling.  In a CTA eight warps sweep while a ninth works through the
+// teacher's list, whose chain of dependent loads would otherwise be most of
+// a short row's time.  Rows may start at any element: the vector part of a row runs
 // from its first 16-byte boundary, the ragged ends element by element.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
 #include "ptx.cuh"
+#include "f32x2.cuh"
 
 #define QLORA_DEV_INDEX 4
 
 namespace qlora {
 
-constexpr int kDiThreads = 512;
-constexpr int kDiWarps = kDiThreads / 32;
+constexpr int kDiWarps = 8;                      // sweep the vocabulary
+constexpr int kDiSweep = kDiWarps * 32;
+constexpr int kDiThreads = kDiSweep + 32;        // and one warp for the teacher's list
 constexpr int kDiMaxTop = 1024;
 constexpr int kDiBatch = 4;            // 16-byte loads in flight per thread
 
@@ -68,31 +72,49 @@ __device__ __forceinline__ float di_exp2(float x) {
   return r;
 }
 
+// A 16-byte chunk of logits: N values as N / 2 pairs of fp32 (packed
+// arithmetic: half the instructions, the same roundings).
+__device__ __forceinline__ uint32_t di_max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 template <typename T> struct DiVec;
 template <> struct DiVec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+  static __device__ __forceinline__ float max(const uint4& v) {
+    // a NaN loses against a number; the sum brings it back
+    uint32_t m = di_max_bf16x2(di_max_bf16x2(v.x, v.y), di_max_bf16x2(v.z, v.w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ void pairs(const uint4& v, f32x2 (&f)[4]) {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = pair2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+  static __device__ __forceinline__ uint4 pack(const f32x2 (&f)[4]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpair2(f[i]);
+      u[i] = pack_bf16x2(x.x, x.y);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
   }
   static __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 };
 template <> struct DiVec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+  static __device__ __forceinline__ float max(const uint4& v) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  static __device__ __forceinline__ void pairs(const uint4& v, f32x2 (&f)[2]) {
+    f[0] = pair2(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = pair2(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  static __device__ __forceinline__ uint4 pack(const f32x2 (&f)[2]) {
+    const float2 x = unpair2(f[0]), y = unpair2(f[1]);
+    return make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
   }
   static __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 };
@@ -119,28 +141,14 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
   return v;
 }
 
-// max and sum over the block, the same in every thread; red holds one float
-// per warp and is free again after the call's last barrier
-__device__ __forceinline__ float di_block_max(float v, float* red) {
+__device__ __forceinline__ float di_warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int i = 1; i < kDiWarps; ++i) v = fmaxf(v, red[i]);
   return v;
 }
-__device__ __forceinline__ float di_block_sum(float v, float* red) {
+__device__ __forceinline__ float di_warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int i = 1; i < kDiWarps; ++i) v += red[i];
   return v;
 }
 
@@ -148,19 +156,20 @@ __device__ __forceinline__ float di_block_sum(float v, float* red) {
 // Otherwise the gradient alone, from a given normaliser (no exchange between
 // the CTAs of a row).
 template <typename T, bool FWD>
-__global__ void __launch_bounds__(kDiThreads, 2) k_distill(const DistillArgs a) {
+__global__ void __launch_bounds__(kDiThreads, 4) k_distill(const DistillArgs a) {
   constexpr int N = DiVec<T>::N;
   __shared__ __align__(16) int s_id[kDiMaxTop];     // vocabulary index, or -1
   __shared__ float s_t[kDiMaxTop];                  // t / tau
   __shared__ float s_p[kDiMaxTop];                  // p
   __shared__ float s_z[kDiMaxTop];                  // the student's logit at the entry
-  __shared__ float red[kDiWarps];
-  __shared__ float2 red2[kDiWarps];
+  __shared__ float2 red[kDiWarps];                  // the warps' (max, sum)
   __shared__ float2 s_mine;                         // this CTA's (max, sum) for its cluster
+  __shared__ int s_empty;                           // no listed entry has weight
 
   const int64_t row = blockIdx.x / a.slices;
   const int slice = static_cast<int>(blockIdx.x % a.slices);   // rank in the cluster (forward)
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const bool teacher = tid >= kDiSweep;
   const T* z = static_cast<const T*>(a.z) + row * a.ldz;
   T* dz = a.dz ? static_cast<T*>(a.dz) + row * a.lddz : nullptr;
 
@@ -168,104 +177,118 @@ __global__ void __launch_bounds__(kDiThreads, 2) k_distill(const DistillArgs a) 
   const uintptr_t za = reinterpret_cast<uintptr_t>(z), da = reinterpret_cast<uintptr_t>(dz);
   int64_t head = static_cast<int64_t>(((16 - (za & 15)) & 15) / sizeof(T));
   if (head > a.vocab || (dz && ((za ^ da) & 15))) head = a.vocab;   // no common 16-byte boundary: element by element
-  const int64_t chunks = (a.vocab - head) / N;
-  const int64_t per = (chunks + a.slices - 1) / a.slices;
-  const int64_t c0 = min(chunks, slice * per), c1 = min(chunks, c0 + per);
+  const int chunks = static_cast<int>((a.vocab - head) / N);
+  const int per = (chunks + a.slices - 1) / a.slices;
+  const int c0 = min(chunks, slice * per), c1 = min(chunks, c0 + per);
   // the ragged ends: [0, head) and [tail, vocab), spread over the slices' threads
-  const int64_t tail = head + chunks * N;
+  const int64_t tail = head + static_cast<int64_t>(chunks) * N;
   const int64_t ragged = head + (a.vocab - tail);
-  const int64_t rag0 = static_cast<int64_t>(slice) * kDiThreads + tid, rstep = static_cast<int64_t>(a.slices) * kDiThreads;
+  const int64_t rag0 = static_cast<int64_t>(slice) * kDiSweep + tid, rstep = static_cast<int64_t>(a.slices) * kDiSweep;
   auto ragged_at = [&](int64_t i) { return i < head ? i : tail + (i - head); };
   const uint4* zv = reinterpret_cast<const uint4*>(z + head);
+  const f32x2 scale = pair2(a.scale2, a.scale2);
 
-  // ---------------------------------------------------------- the teacher
-  float tmax = -INFINITY;
-  bool bad = false;
-  for (int j = tid; j < a.top; j += kDiThreads) {
-    const int64_t e = row * a.top + j;
-    const int64_t id = a.ids64 ? static_cast<const int64_t*>(a.ids)[e] : static_cast<const int32_t*>(a.ids)[e];
-    const float t = (a.t_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.t)[e])
-                              : static_cast<const float*>(a.t)[e]) / a.tau;
-    const bool ok = id >= 0 && id < a.vocab;
-    bad |= id >= a.vocab;
-    s_id[j] = ok ? static_cast<int>(id) : -1;
-    s_t[j] = ok ? t : -INFINITY;
-    s_z[j] = ok ? static_cast<float>(z[id]) : 0.0f;
-    if (ok) tmax = fmaxf(tmax, t);
-  }
-  if (tid < 4 && a.top + tid < kDiMaxTop) s_id[a.top + tid] = -1;   // the scan below reads whole groups of four
-  if (bad && a.status) atomicOr(a.status, QLORA_DEV_INDEX);
-  tmax = di_block_max(tmax, red);
-  const float tref = tmax == -INFINITY ? 0.0f : tmax;
-  float tsum = 0.0f;
-  for (int j = tid; j < a.top; j += kDiThreads) {
-    const float e = s_id[j] >= 0 ? expf(s_t[j] - tref) : 0.0f;
-    s_p[j] = e;
-    tsum += e;
-  }
-  tsum = di_block_sum(tsum, red);
-  const bool empty = tsum == 0.0f;       // nothing listed (a NaN is not nothing)
-  const float tinv = empty ? 0.0f : 1.0f / tsum;
-  for (int j = tid; j < a.top; j += kDiThreads) s_p[j] *= tinv;
-  const float weight = a.weight ? a.weight[row] : 1.0f;
-
-  // ------------------------------------------------------ the normaliser
-  // q = exp2((z - ref) scale2 - l2)
-  float ref, l2;
-  if (FWD) {
-    DiSum acc{-INFINITY, 0.0f};
+  DiSum acc{-INFINITY, 0.0f};
+  float tref = 0.0f, tsum = 0.0f;
+  if (teacher) {
+    // -------------------------------------------------------- the teacher
+    float tmax = -INFINITY;
+    bool bad = false;
+    for (int j = lane; j < a.top; j += 32) {
+      const int64_t e = row * a.top + j;
+      const int64_t id = a.ids64 ? static_cast<const int64_t*>(a.ids)[e] : static_cast<const int32_t*>(a.ids)[e];
+      const float t = (a.t_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.t)[e])
+                                : static_cast<const float*>(a.t)[e]) / a.tau;
+      const bool ok = id >= 0 && id < a.vocab;
+      bad |= id >= a.vocab;
+      s_id[j] = ok ? static_cast<int>(id) : -1;
+      s_t[j] = ok ? t : -INFINITY;
+      s_z[j] = ok ? static_cast<float>(z[id]) : 0.0f;
+      if (ok) tmax = fmaxf(tmax, t);
+    }
+    if (lane < 4 && a.top + lane < kDiMaxTop) s_id[a.top + lane] = -1;   // the scan below reads whole groups of four
+    if (bad && a.status) atomicOr(a.status, QLORA_DEV_INDEX);
+    tmax = di_warp_max(tmax);
+    tref = tmax == -INFINITY ? 0.0f : tmax;
+    for (int j = lane; j < a.top; j += 32) {
+      const float e = s_id[j] >= 0 ? expf(s_t[j] - tref) : 0.0f;
+      s_p[j] = e;
+      tsum += e;
+    }
+    tsum = di_warp_sum(tsum);
+    const float tinv = tsum == 0.0f ? 0.0f : 1.0f / tsum;              // (a NaN is not nothing)
+    for (int j = lane; j < a.top; j += 32) s_p[j] *= tinv;
+    if (lane == 0) s_empty = tsum == 0.0f ? 1 : 0;
+  } else if (FWD) {
+    // -------------------------------------------------------- the sweep
+    // `m`: a batch's maximum; `each(max)`: its sum of exponentials
     auto take = [&](float m, auto&& each) {
-      // `m`: the batch's maximum; `each(max)`: its sum of exponentials
       if (m > acc.max) {
         if (acc.max != -INFINITY) acc.sum *= di_exp2((acc.max - m) * a.scale2);
         acc.max = m;
       }
       acc.sum += each(di_ref(acc.max));
     };
-    for (int64_t c = c0 + tid; c < c1; c += kDiBatch * kDiThreads) {
+    auto chunk_sum = [&](const uint4& v, f32x2 neg, f32x2& s2) {
+      f32x2 f[N / 2];
+      DiVec<T>::pairs(v, f);
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) {
+        const float2 x = unpair2(mul2(add2(f[e], neg), scale));
+        s2 = add2(s2, pair2(di_exp2(x.x), di_exp2(x.y)));
+      }
+    };
+    int c = c0 + tid;
+    for (; c + (kDiBatch - 1) * kDiSweep < c1; c += kDiBatch * kDiSweep) {
       uint4 v[kDiBatch];
 #pragma unroll
-      for (int b = 0; b < kDiBatch; ++b) {
-        const int64_t at = c + b * kDiThreads;
-        v[b] = zv[at < c1 ? at : c];     // past the end: the batch's first chunk again, not summed
-      }
-      float m = -INFINITY;
+      for (int b = 0; b < kDiBatch; ++b) v[b] = zv[c + b * kDiSweep];
+      float m = DiVec<T>::max(v[0]);
 #pragma unroll
-      for (int b = 0; b < kDiBatch; ++b) {
-        float f[N];
-        DiVec<T>::unpack(v[b], f);
-#pragma unroll
-        for (int e = 0; e < N; ++e) m = fmaxf(m, f[e]);
-      }
+      for (int b = 1; b < kDiBatch; ++b) m = fmaxf(m, DiVec<T>::max(v[b]));
       take(m, [&](float top) {
-        float s = 0.0f;
+        f32x2 s2 = 0;
+        const f32x2 neg = pair2(-top, -top);
 #pragma unroll
-        for (int b = 0; b < kDiBatch; ++b) {
-          if (c + b * kDiThreads < c1) {
-            float f[N];
-            DiVec<T>::unpack(v[b], f);
-#pragma unroll
-            for (int e = 0; e < N; ++e) s += di_exp2((f[e] - top) * a.scale2);
-          }
-        }
-        return s;
+        for (int b = 0; b < kDiBatch; ++b) chunk_sum(v[b], neg, s2);
+        const float2 s = unpair2(s2);
+        return s.x + s.y;
+      });
+    }
+    for (; c < c1; c += kDiSweep) {
+      const uint4 v = zv[c];
+      take(fmaxf(DiVec<T>::max(v), -INFINITY), [&](float top) {
+        f32x2 s2 = 0;
+        chunk_sum(v, pair2(-top, -top), s2);
+        const float2 s = unpair2(s2);
+        return s.x + s.y;
       });
     }
     for (int64_t i = rag0; i < ragged; i += rstep) {
       const float f = static_cast<float>(z[ragged_at(i)]);
       take(fmaxf(f, -INFINITY), [&](float top) { return di_exp2((f - top) * a.scale2); });
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const DiSum other{__shfl_xor_sync(0xFFFFFFFFu, acc.max, o), __shfl_xor_sync(0xFFFFFFFFu, acc.sum, o)};
-      // the lower lane's part first in both lanes, so that both hold the same sum
-      acc = (tid & o) ? di_merge(other, acc, a.scale2) : di_merge(acc, other, a.scale2);
-    }
-    if ((tid & 31) == 0) red2[tid >> 5] = make_float2(acc.max, acc.sum);
+    // the warp's sum: the largest maximum, then every lane's part against it
+    const float m = di_warp_max(acc.max);
+    const float part = acc.max == -INFINITY ? acc.sum : acc.sum * di_exp2((acc.max - di_ref(m)) * a.scale2);
+    const float sum = di_warp_sum(part);
+    if (lane == 0) red[tid >> 5] = make_float2(m, sum);
+  }
+
+  const float weight = a.weight ? a.weight[row] : 1.0f;
+  // q = exp2((z - ref) scale2 - l2)
+  float ref, l2;
+  if (FWD) {
     __syncthreads();
-    acc = DiSum{red2[0].x, red2[0].y};
+    acc = DiSum{red[0].x, red[0].y};
 #pragma unroll
-    for (int i = 1; i < kDiWarps; ++i) acc = di_merge(acc, DiSum{red2[i].x, red2[i].y}, a.scale2);
+    for (int i = 1; i < kDiWarps; ++i) acc.max = fmaxf(acc.max, red[i].x);
+    {
+      const float2 mine = red[lane % kDiWarps];
+      float part = lane < kDiWarps ? mine.y : 0.0f;
+      if (lane < kDiWarps && mine.x != -INFINITY) part *= di_exp2((mine.x - di_ref(acc.max)) * a.scale2);
+      acc.sum = di_warp_sum(part);
+    }
     if (a.slices > 1) {
       if (tid == 0) s_mine = make_float2(acc.max, acc.sum);
       cluster_sync();
@@ -279,73 +302,82 @@ __global__ void __launch_bounds__(kDiThreads, 2) k_distill(const DistillArgs a) 
     ref = di_ref(acc.max);
     l2 = log2f(acc.sum);
 
-    if (slice == 0) {
-      const float zlog = logf(acc.sum);
+    if (teacher && slice == 0) {
+      const float zlog = logf(acc.sum), tlog = logf(tsum);
       float kl = 0.0f;
-      const float tlog = logf(tsum);
-      for (int j = tid; j < a.top; j += kDiThreads) {
+      for (int j = lane; j < a.top; j += 32) {
         const float p = s_p[j];
         // p = 0 contributes nothing even where q = 0; a NaN p stays
         if (!(p == 0.0f)) kl += p * (((s_t[j] - tref) - tlog) - ((s_z[j] - ref) / a.tau - zlog));
       }
-      kl = di_block_sum(kl, red);
-      if (tid == 0) {
+      kl = di_warp_sum(kl);
+      if (lane == 0) {
         const float f = weight * (a.tau * a.tau);
-        a.loss[row] = (empty || weight == 0.0f) ? 0.0f : f * kl;
+        a.loss[row] = (s_empty || weight == 0.0f) ? 0.0f : f * kl;
         if (a.lse) a.lse[row] = ref / a.tau + zlog;
       }
     }
   } else {
     ref = a.lse_in[row] * a.tau;
     l2 = 0.0f;
+    if (a.dz == a.z) __syncthreads();    // the entries' logits are taken before dz overwrites them
   }
 
   // --------------------------------------------------------- the gradient
   if (dz) {
     float f = weight * a.tau;
     if (!FWD && a.grad) f *= a.grad[row];
-    const bool none = empty || weight == 0.0f || f == 0.0f;
     uint4* dv = reinterpret_cast<uint4*>(dz + head);
-    __syncthreads();                     // s_p, and the entries' logits before dz may overwrite z
-    if (none) {
-      for (int64_t c = c0 + tid; c < c1; c += kDiThreads) dv[c] = make_uint4(0, 0, 0, 0);
+    auto zeros = [&]() {
+      for (int c = c0 + tid; c < c1; c += kDiSweep) dv[c] = make_uint4(0, 0, 0, 0);
       for (int64_t i = rag0; i < ragged; i += rstep) DiVec<T>::store(dz + ragged_at(i), 0.0f);
+    };
+    const bool none = weight == 0.0f || f == 0.0f || (FWD && s_empty);
+    if (none) {
+      if (!teacher) zeros();
     } else {
-      for (int64_t c = c0 + tid; c < c1; c += kDiBatch * kDiThreads) {
-        uint4 v[kDiBatch];
+      if (!teacher) {
+        const f32x2 neg = pair2(-ref, -ref), nl2 = pair2(-l2, -l2), ff = pair2(f, f);
+        for (int c = c0 + tid; c < c1; c += kDiBatch * kDiSweep) {
+          uint4 v[kDiBatch];
 #pragma unroll
-        for (int b = 0; b < kDiBatch; ++b) {
-          const int64_t at = c + b * kDiThreads;
-          if (at < c1) v[b] = zv[at];
-        }
+          for (int b = 0; b < kDiBatch; ++b)
+            if (c + b * kDiSweep < c1) v[b] = zv[c + b * kDiSweep];
 #pragma unroll
-        for (int b = 0; b < kDiBatch; ++b) {
-          const int64_t at = c + b * kDiThreads;
-          if (at < c1) {
-            float g[N];
-            DiVec<T>::unpack(v[b], g);
+          for (int b = 0; b < kDiBatch; ++b) {
+            if (c + b * kDiSweep < c1) {
+              f32x2 g[N / 2];
+              DiVec<T>::pairs(v[b], g);
 #pragma unroll
-            for (int e = 0; e < N; ++e) g[e] = f * di_exp2(fmaf(g[e] - ref, a.scale2, -l2));
-            dv[at] = DiVec<T>::pack(g);
+              for (int e = 0; e < N / 2; ++e) {
+                const float2 x = unpair2(fma2(add2(g[e], neg), scale, nl2));
+                g[e] = mul2(pair2(di_exp2(x.x), di_exp2(x.y)), ff);
+              }
+              dv[c + b * kDiSweep] = DiVec<T>::pack(g);
+            }
           }
         }
-      }
-      for (int64_t i = rag0; i < ragged; i += rstep) {
-        const int64_t at = ragged_at(i);
-        DiVec<T>::store(dz + at, f * di_exp2(fmaf(static_cast<float>(z[at]) - ref, a.scale2, -l2)));
+        for (int64_t i = rag0; i < ragged; i += rstep) {
+          const int64_t at = ragged_at(i);
+          DiVec<T>::store(dz + at, f * di_exp2(fmaf(static_cast<float>(z[at]) - ref, a.scale2, -l2)));
+        }
       }
       __syncthreads();                   // the sweep's writes come before the listed entries'
+      if (!FWD && s_empty) {             // (the backward learns it from the teacher's warp only here)
+        if (!teacher) zeros();
+        return;
+      }
       for (int j = tid; j < a.top; j += kDiThreads) {
         const int id = s_id[j];
         // the CTA that swept the entry's place writes it
         bool mine = false;
         if (id >= 0) {
           if (id >= head && id < tail) {
-            const int64_t c = (id - head) / N;
+            const int c = static_cast<int>((id - head) / N);
             mine = c >= c0 && c < c1;
           } else {
             const int64_t i = id < head ? id : head + (id - tail);
-            mine = (i / kDiThreads) % a.slices == slice;
+            mine = (i / kDiSweep) % a.slices == slice;
           }
         }
         if (mine) {

@@ -28,6 +28,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 #include "ptx.cuh"
+#include "f32x2.cuh"
 
 namespace qlora {
 
@@ -411,35 +412,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 constexpr int kLnMaxStages = 8;
 
-// Two fp32 values in one register pair (each operation rounds each value as
-// its scalar form does): the ring kernels' arithmetic per byte is what keeps
-// them from the memory's rate, and pairs halve its instructions.
-typedef uint64_t f32x2;
-__device__ __forceinline__ f32x2 pair2(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpair2(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
+// The ring kernels' arithmetic per byte is what keeps them from the memory's
+// rate: packed pairs of fp32 halve its instructions.
 // VEC elements from shared memory as pairs; zeros past the last column
 template <typename T, int VEC>
 __device__ __forceinline__ void ln_pairs(const T* p, bool in, f32x2 (&v)[VEC / 2]) {

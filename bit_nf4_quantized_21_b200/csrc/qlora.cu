@@ -1721,10 +1721,10 @@ qlora_status check_distill(const void* Z, int64_t ldz, int64_t rows, int64_t voc
   return QLORA_OK;
 }
 
-// CTAs per row: enough to give every SM two CTAs, as long as a slice keeps
-// a few thousand logits (below that a CTA is mostly its fixed cost).
+// CTAs per row: enough to give every SM its four CTAs, as long as a slice
+// keeps a few thousand logits (below that a CTA is mostly its fixed cost).
 int distill_slices(int64_t rows, int64_t vocab) {
-  const int64_t ctas = 2LL * std::max(1, sm_count());
+  const int64_t ctas = 4LL * std::max(1, sm_count());
   int s = 1;
   while (s < 8 && rows * s < ctas && vocab / (2 * s) >= 4096) s *= 2;
   return s;
