@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kDiThreads, 4) k_distill(const DistillArgs a) 
                 const float2 x = unpair2(fma2(add2(g[e], neg), scale, nl2));
                 g[e] = mul2(pair2(di_exp2(x.x), di_exp2(x.y)), ff);
               }
-              dv[c + b * kDiSweep] = DiVec<T>::pack(g);
+              __stcs(dv + c + b * kDiSweep, DiVec<T>::pack(g));   // (leaves L2 to the logits that are read twice)
             }
           }
         }

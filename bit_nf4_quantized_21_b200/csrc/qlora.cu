@@ -1721,18 +1721,22 @@ qlora_status check_distill(const void* Z, int64_t ldz, int64_t rows, int64_t voc
   return QLORA_OK;
 }
 
+constexpr int64_t kDiL2Rows = int64_t(64) << 20;
 // CTAs per row: enough to give every SM its four CTAs, as long as a slice
 // keeps a few thousand logits (below that a CTA is mostly its fixed cost).
-int distill_slices(int64_t rows, int64_t vocab) {
+// With the gradient a row is read twice: rows in flight are then also kept to
+// what L2 holds beside the gradient's writes.
+int distill_slices(int64_t rows, int64_t vocab, int64_t twice_bytes) {
   const int64_t ctas = 4LL * std::max(1, sm_count());
   int s = 1;
+  while (s < 8 && std::min(rows, ctas / s) * twice_bytes > kDiL2Rows && vocab / (2 * s) >= 4096) s *= 2;
   while (s < 8 && rows * s < ctas && vocab / (2 * s) >= 4096) s *= 2;
   return s;
 }
 
 template <bool FWD>
 qlora_status run_distill(DistillArgs& a, qlora_dtype dtype, cudaStream_t cs) {
-  a.slices = distill_slices(a.rows, a.vocab);
+  a.slices = distill_slices(a.rows, a.vocab, FWD && a.dz ? a.vocab * static_cast<int64_t>(dtype_size(dtype)) : 0);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows * a.slices));
   cfg.blockDim = dim3(kDiThreads);
