@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -612,6 +613,15 @@ class FP8Matrix:
         return self.codes.numel() + 4 * self.scale.numel()
 
 
+def _fp8_scratch(X: torch.Tensor, rows: int, cols: int):
+    """(descriptor, owner) of quantised activations [rows, cols] that live for one call."""
+    kb = -(-cols // 128)
+    codes = rows * kb * 128
+    buf = X.new_empty(codes + 4 * kb * rows, dtype=torch.uint8)
+    p = buf.data_ptr()
+    return FP8MatrixC(rows, cols, kb * 128, 1, 0, p, p + codes), buf
+
+
 def qlora_fp8_sizes(rows: int, cols: int, block_rows: int = 128) -> tuple[int, int]:
     c, s = ctypes.c_size_t(), ctypes.c_size_t()
     _check(lib().qlora_fp8_sizes(rows, cols, block_rows, ctypes.byref(c), ctypes.byref(s)), "qlora_fp8_sizes")
@@ -642,25 +652,32 @@ def qlora_fp8_quantize(X: torch.Tensor, out: FP8Matrix | None = None, block_rows
 
 
 def _fp8_linear(where, X, Wq, out, out_dtype, Xq, d_status, stream, in_cols, out_cols):
-    with _on(stream, Wq.codes, Wq.scale, out, d_status,
-             *((X.codes, X.scale) if isinstance(X, FP8Matrix) else (X,)),
+    quantised = isinstance(X, FP8Matrix)
+    with _on(stream, Wq.codes, Wq.scale, out, d_status, *((X.codes, X.scale) if quantised else (X,)),
              *(() if Xq is None else (Xq.codes, Xq.scale))):
-        if isinstance(X, FP8Matrix):
+        keep = None
+        if quantised:
             if Xq is not None:
                 raise ValueError("already quantised activations need no scratch")
-            p, dt, ld, Xq = None, QLORA_F32, 0, X
+            p, dt, ld, rows, cx = None, QLORA_F32, 0, X.rows, X.c()
         else:
             p, ld = _matrix(X, "activations", cols=in_cols)
             dt = _dtype(X, "activations")
+            rows = X.shape[0]
             if Xq is None:
-                Xq = empty_fp8(X.shape[0], in_cols, X.device, 1)
-            elif Xq.rows != X.shape[0]:
+                cx, keep = _fp8_scratch(X, rows, in_cols)
+            elif Xq.rows != rows:
                 raise ValueError("the scratch must have the activations' rows")
+            else:
+                cx = Xq.c()
         if out is None:
-            out = Xq.codes.new_empty((Xq.rows, out_cols), dtype=out_dtype)
-        o, ldo = _matrix(out, "output", Xq.rows, out_cols)
-        _check(getattr(lib(), where)(p, dt, ld, ctypes.byref(Wq.c()), ctypes.byref(Xq.c()), o, _dtype(out, "output"),
-                                     ldo, _ptr(d_status), _current(out)), where)
+            out = Wq.codes.new_empty((rows, out_cols), dtype=out_dtype)
+            o, ldo = out.data_ptr(), out_cols
+        else:
+            o, ldo = _matrix(out, "output", rows, out_cols)
+        _check(getattr(lib(), where)(p, dt, ld, ctypes.byref(Wq.c()), ctypes.byref(cx), o, _dtype(out, "output"), ldo,
+                                     _ptr(d_status), _current(out)), where)
+        del keep                        # (its memory is reused on this stream only)
     return out
 
 
@@ -681,16 +698,13 @@ def qlora_fp8_linear_bwd(dY: torch.Tensor | FP8Matrix, Wq: FP8Matrix, dX: torch.
 
 # ------------------------------------------------------------------- layer norm
 
+@functools.lru_cache(maxsize=256)
 def qlora_layernorm_workspace_bytes(rows: int, cols: int) -> int:
     return int(lib().qlora_layernorm_workspace_bytes(rows, cols))
 
 
-def _params(cols: int, *ps):
-    """(pointers, dtype) of weight and bias, which share one type."""
-    given = [p for p in ps if p is not None]
-    if any(p.dtype != given[0].dtype for p in given):
-        raise ValueError("weight and bias must have one type")
-    return [_vector(p, "weight and bias", cols) for p in ps], _dtype(given[0], "weight and bias") if given else QLORA_F32
+def _param(p: torch.Tensor | None, cols: int) -> int | None:
+    return None if p is None else _vector(p, "weight and bias", cols)
 
 
 def qlora_layernorm_fwd(X: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
@@ -700,17 +714,22 @@ def qlora_layernorm_fwd(X: torch.Tensor, weight: torch.Tensor | None = None, bia
     with _on(stream, X, weight, bias, Y, mean, rstd, d_status):
         x, ldx = _matrix(X, "X")
         rows, cols = X.shape
-        (w, b), wdt = _params(cols, weight, bias)
+        like = weight if weight is not None else bias
+        if weight is not None and bias is not None and weight.dtype != bias.dtype:
+            raise ValueError("weight and bias must have one type")
         if Y is None:
             Y = torch.empty_like(X, memory_format=torch.contiguous_format)
+            y, ldy = Y.data_ptr(), cols
         elif Y.dtype != X.dtype:
             raise ValueError("Y has X's type")
-        y, ldy = _matrix(Y, "Y", rows, cols)
+        else:
+            y, ldy = _matrix(Y, "Y", rows, cols)
         if mean is None:
             mean = X.new_empty(rows, dtype=torch.float32)
         if rstd is None:
             rstd = torch.empty_like(mean)
-        _check(lib().qlora_layernorm_fwd(x, ldx, rows, cols, _dtype(X, "X"), w, b, wdt, float(eps), y, ldy,
+        _check(lib().qlora_layernorm_fwd(x, ldx, rows, cols, _dtype(X, "X"), _param(weight, cols), _param(bias, cols),
+                                         QLORA_F32 if like is None else _dtype(like, "weight and bias"), eps, y, ldy,
                                          _vector(mean, "mean", rows, torch.float32),
                                          _vector(rstd, "rstd", rows, torch.float32), _ptr(d_status), _current(X)),
                "qlora_layernorm_fwd")
@@ -726,33 +745,36 @@ def qlora_layernorm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor 
         x, ldx = _matrix(X, "X")
         rows, cols = X.shape
         dy, lddy = _matrix(dY, "dY", rows, cols)
-        (w,), wdt = _params(cols, weight)
         if dX is None:
             dX = torch.empty_like(X, memory_format=torch.contiguous_format)
+            dx, lddx = dX.data_ptr(), cols
+        else:
+            dx, lddx = _matrix(dX, "dX", rows, cols)
         if dY.dtype != X.dtype or dX.dtype != X.dtype:
             raise ValueError("dY and dX have X's type")
-        dx, lddx = _matrix(dX, "dX", rows, cols)
         if want_params:
             gt = dweight.dtype if dweight is not None else dbias.dtype if dbias is not None else grad_dtype
             if dweight is None:
                 dweight = X.new_empty(cols, dtype=gt)
             if dbias is None:
                 dbias = torch.empty_like(dweight, dtype=gt)
-        gdt = QLORA_F32
-        for g in (dweight, dbias):
-            if g is not None:
-                gdt = _dtype(g, "dweight and dbias")
         if dweight is not None and dbias is not None and dweight.dtype != dbias.dtype:
             raise ValueError("dweight and dbias must have one type")
+        grad = dweight if dweight is not None else dbias
         ws, ws_bytes = None, 0
-        if dweight is not None or dbias is not None:
+        if grad is not None:
             if workspace is None:
-                workspace = X.new_empty(max(qlora_layernorm_workspace_bytes(rows, cols), 16), dtype=torch.uint8)
-            ws, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-        _check(lib().qlora_layernorm_bwd(dy, lddy, x, ldx, rows, cols, _dtype(X, "X"), w, wdt,
+                ws_bytes = max(qlora_layernorm_workspace_bytes(rows, cols), 16)
+                workspace = X.new_empty(ws_bytes, dtype=torch.uint8)
+                ws = workspace.data_ptr()
+            else:
+                ws, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+        _check(lib().qlora_layernorm_bwd(dy, lddy, x, ldx, rows, cols, _dtype(X, "X"), _param(weight, cols),
+                                         QLORA_F32 if weight is None else _dtype(weight, "weight and bias"),
                                          _vector(mean, "mean", rows, torch.float32),
                                          _vector(rstd, "rstd", rows, torch.float32), dx, lddx,
-                                         _vector(dweight, "dweight", cols), _vector(dbias, "dbias", cols), gdt, ws,
+                                         _vector(dweight, "dweight", cols), _vector(dbias, "dbias", cols),
+                                         QLORA_F32 if grad is None else _dtype(grad, "dweight and dbias"), ws,
                                          ws_bytes, _ptr(d_status), _current(X)), "qlora_layernorm_bwd")
     return dX, dweight, dbias
 
