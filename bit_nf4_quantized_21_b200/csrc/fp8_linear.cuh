@@ -562,12 +562,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           if (leader) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * kF8SlotBytes);
           const uint32_t dst = smem_u32(base) + s * kF8SlotBytes;
           // (a skipped load leaves the slot's wait to run out: bounded, the launch aborts)
-          if (QLORA_CHECK((s + 1) * kF8SlotBytes <= kF8OffStage && m0 >= 0 && c0 >= 0, 201)) {
+          const bool skip = it == 0 && blockIdx.x == 0 && qlora_stalled();
+          if (!skip && QLORA_CHECK((s + 1) * kF8SlotBytes <= kF8OffStage && m0 >= 0 && c0 >= 0, 201)) {
             if (MODE == 0) tma_load_2d_pair(dst + kF8OpBytes, &tm_w, fb, kb * kF8Block, c0);
             else tma_load_2d_pair(dst + kF8OpBytes, &tm_w, fb, c0, kb * kF8Block);
-            if (waiting) { griddep_wait(); waiting = false; }
-            tma_load_2d_pair(dst, &tm_act, fb, kb * kF8Block, m0);
           }
+          if (waiting) { griddep_wait(); waiting = false; }
+          if (!skip && QLORA_CHECK((s + 1) * kF8SlotBytes <= kF8OffStage && m0 >= 0, 201))
+            tma_load_2d_pair(dst, &tm_act, fb, kb * kF8Block, m0);
         }
       }
       if (*abort_flag && leader) {
@@ -615,6 +617,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
               break;
             }
             float* slot = reinterpret_cast<float*>(base + kF8OffScale + (it % kF8ScaleRing) * kF8ScaleBytes);
+            QLORA_CHECK_ONLY(kF8OffScale + (it % kF8ScaleRing + 1) * kF8ScaleBytes <= kF8OffBar, 203);
 #pragma unroll
             for (int i = 0; i < 4; ++i) slot[lane + 32 * i] = a[b][i];
             if (lane < 2) slot[128 + lane] = w[b];
@@ -681,11 +684,12 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t buf = 2 * (it & 1) + h;
-          if (!ahead && !mbar_wait(filled + 8 * buf, (it >> 1) & 1, abort_flag, args.status)) {
+          // (votes: the lanes of a warp take the same way out of an aborted launch)
+          if (!__all_sync(0xFFFFFFFFu, ahead) &&
+              !__all_sync(0xFFFFFFFFu, mbar_wait(filled + 8 * buf, (it >> 1) & 1, abort_flag, args.status))) {
             live = false;
             break;
           }
-          __syncwarp();
           tc_fence_after();
           uint32_t r[64];
           tmem_ld32(taddr + 128u * buf, r);
@@ -716,6 +720,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         if (!args.out_f32 && b >= 2) break;
         if (lane == 0) bulk_wait_read();                           // the box before has been read
         __syncwarp();
+        QLORA_CHECK_ONLY(kF8OffStage + (warp + 1) * kF8StageBytes <= kF8OffScale, 202);
         uint8_t* line = stage + lane * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {

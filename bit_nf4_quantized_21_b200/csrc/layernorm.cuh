@@ -411,6 +411,15 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 constexpr int kLnMaxStages = 8;
+// After a wait that gave up: the loads still under way land before the block
+// can exit (bounded).  By the thread that asked for them.
+__device__ __forceinline__ void ln_drain(uint64_t* full, int stages, int64_t asked) {
+  for (int64_t i = asked > stages ? asked - stages : 0; i < asked; ++i) {
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(smem_u32(&full[i % stages]), static_cast<uint32_t>((i / stages) & 1)) &&
+           global_ns() - t0 < qlora_drain_limit()) {}
+  }
+}
 
 // The ring kernels' arithmetic per byte is what keeps them from the memory's
 // rate: packed pairs of fp32 halve its instructions.
@@ -463,11 +472,14 @@ __global__ void __launch_bounds__(GROUP, 1024 / GROUP) k_ln_fwd_ring(const LnArg
   __syncthreads();
   auto ask = [&](int64_t i, int s) {       // row i of this block into slot s
     mbar_arrive_expect_tx(smem_u32(&full[s]), row_bytes);
+    if (i == 0 && blockIdx.x == 0 && qlora_stalled()) return;   // the test hook: this row never comes
     bulk_load(smem_u32(ring) + s * row_bytes, static_cast<const T*>(a.x) + (blockIdx.x + i * gridDim.x) * a.ldx, row_bytes,
               smem_u32(&full[s]));
   };
+  int64_t asked = 0;                       // rows asked for, by thread 0
+  bool came = true;                        // every row so far
   if (t == 0)
-    for (int i = 0; i < a.stages && i < mine; ++i) ask(i, i);
+    for (; asked < a.stages && asked < mine; ++asked) ask(asked, static_cast<int>(asked));
   f32x2 w[PER][H], b[PER][H];
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
@@ -482,8 +494,10 @@ __global__ void __launch_bounds__(GROUP, 1024 / GROUP) k_ln_fwd_ring(const LnArg
   uint32_t parity = 0;
   for (int64_t i = 0; i < mine; ++i) {
     const int64_t row = blockIdx.x + i * gridDim.x;
-    // (a wait that gives up says so in *status; the rest of the launch runs out quickly)
-    mbar_wait(smem_u32(&full[s]), parity, &abort_word, a.status);
+    // A wait that gives up says so in *status.  Every later wait then gives up
+    // at once, and no more rows are asked for (a slot whose row has not come
+    // is still in its old phase), so the launch runs out quickly.
+    came = mbar_wait(smem_u32(&full[s]), parity, &abort_word, a.status) && came;
     const T* src = reinterpret_cast<const T*>(ring + s * row_bytes);
     f32x2 v[PER][H], acc = 0;
 #pragma unroll
@@ -495,7 +509,7 @@ __global__ void __launch_bounds__(GROUP, 1024 / GROUP) k_ln_fwd_ring(const LnArg
     }
     float2 sum = unpair2(acc);
     const float mean = ln_group_sum1<GROUP>(sum.x + sum.y, red[0]) * inv;
-    if (t == 0 && i + a.stages < mine) ask(i + a.stages, s);
+    if (t == 0 && came && asked < mine) ask(asked++, s);
     const f32x2 neg = pair2(-mean, -mean);
     acc = 0;
 #pragma unroll
@@ -527,6 +541,7 @@ __global__ void __launch_bounds__(GROUP, 1024 / GROUP) k_ln_fwd_ring(const LnArg
     }
     if (++s == a.stages) { s = 0; parity ^= 1; }
   }
+  if (t == 0 && *const_cast<volatile int*>(&abort_word)) ln_drain(full, a.stages, asked);
 }
 
 template <typename T, int GROUP, int PER, bool FULL>
@@ -550,11 +565,14 @@ __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
     const int64_t row = blockIdx.x + i * gridDim.x;
     const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(ring) + 2 * s * row_bytes;
     mbar_arrive_expect_tx(bar, 2 * row_bytes);
+    if (i == 0 && blockIdx.x == 0 && qlora_stalled()) return;   // the test hook: these rows never come
     bulk_load(dst, static_cast<const T*>(a.x) + row * a.ldx, row_bytes, bar);
     bulk_load(dst + row_bytes, static_cast<const T*>(a.dy) + row * a.lddy, row_bytes, bar);
   };
+  int64_t asked = 0;                       // rows asked for, by thread 0
+  bool came = true;                        // every row so far
   if (t == 0)
-    for (int i = 0; i < a.stages && i < mine; ++i) ask(i, i);
+    for (; asked < a.stages && asked < mine; ++asked) ask(asked, static_cast<int>(asked));
   f32x2 w[PER][H], dw[PER][H], db[PER][H];
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
@@ -571,7 +589,7 @@ __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
     const int64_t row = blockIdx.x + i * gridDim.x;
     const int64_t next = i + 1 < mine ? row + gridDim.x : row;
     const float mu_next = a.mean[next], rs_next = a.rstd[next];
-    mbar_wait(smem_u32(&full[s]), parity, &abort_word, a.status);
+    came = mbar_wait(smem_u32(&full[s]), parity, &abort_word, a.status) && came;   // (as in the forward)
     const T* xs = reinterpret_cast<const T*>(ring + 2 * s * row_bytes);
     const T* ds = reinterpret_cast<const T*>(ring + (2 * s + 1) * row_bytes);
     const f32x2 neg = pair2(-mu, -mu), scale = pair2(rs, rs);
@@ -594,7 +612,7 @@ __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
     }
     const float2 p = unpair2(sg), q = unpair2(sgx);
     const float2 sum = ln_group_sum<GROUP>(make_float2(p.x + p.y, q.x + q.y), red[i & 1]);
-    if (t == 0 && i + a.stages < mine) ask(i + a.stages, s);
+    if (t == 0 && came && asked < mine) ask(asked++, s);
     const float m1 = -sum.x * inv, m2 = -sum.y * inv;
     const f32x2 n1 = pair2(m1, m1), n2 = pair2(m2, m2);
     T* dx = static_cast<T*>(a.dx) + row * a.lddx;
@@ -611,6 +629,7 @@ __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
     rs = rs_next;
     if (++s == a.stages) { s = 0; parity ^= 1; }
   }
+  if (t == 0 && *const_cast<volatile int*>(&abort_word)) ln_drain(full, a.stages, asked);
   griddep_launch_dependents();             // k_ln_finish
   if (a.part) {
     float fw[PER][VEC], fb[PER][VEC];

@@ -77,6 +77,16 @@ __device__ __forceinline__ uint64_t qlora_drain_limit() {
   return w < 200000000ull ? w : 200000000ull;
 }
 
+// Test hook (qlora_debug_inject_stall): when set, CTA 0 of the first problem
+// of every adapter-product launch, of every FP8 GEMM and of every layer norm
+// through the ring withholds the loads of its first stage, so that the
+// bounded wait on them runs out and the launch takes its timeout path (status
+// bit, early exit, TMEM released).
+__device__ int g_qlora_inject_stall = 0;
+__device__ __forceinline__ bool qlora_stalled() {
+  return *reinterpret_cast<volatile int*>(&g_qlora_inject_stall) != 0;
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -1617,7 +1617,7 @@ qlora_status qlora_layernorm_fwd(const void* X, int64_t ldx, int64_t rows, int64
   if (rows == 0) return QLORA_OK;
   const size_t es = dtype_size(dtype), wsz = dtype_size(w_dtype);
   if (!X || !Y || !aligned_to(X, es) || !aligned_to(Y, es) || !aligned_to(weight, wsz) || !aligned_to(bias, wsz) ||
-      !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4) || (Y == X && ldy != ldx))
     return QLORA_ERR_INVALID_ARG;
   LnArgs a{};
   a.x = X; a.ldx = ldx; a.w = weight; a.b = bias; a.w_bf16 = w_dtype == QLORA_BF16 ? 1 : 0;
@@ -1650,7 +1650,8 @@ qlora_status qlora_layernorm_bwd(const void* dY, int64_t lddy, const void* X, in
   if (!aligned_to(weight, dtype_size(w_dtype)) || !aligned_to(dweight, gs) || !aligned_to(dbias, gs))
     return QLORA_ERR_INVALID_ARG;
   if (rows > 0 && (!dY || !X || !dX || !mean || !rstd || !aligned_to(dY, es) || !aligned_to(X, es) ||
-                   !aligned_to(dX, es) || !aligned_to(mean, 4) || !aligned_to(rstd, 4)))
+                   !aligned_to(dX, es) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) || (dX == X && lddx != ldx) ||
+                   (dX == dY && lddx != lddy)))
     return QLORA_ERR_INVALID_ARG;
   const bool want = dweight || dbias;
   if (want && rows > 0) {

@@ -181,12 +181,6 @@ __device__ __forceinline__ void sk_grad_out(const SkinnyArgs& a, int64_t p, int 
   }
 }
 
-// Test hook (qlora_debug_inject_stall): when set, CTA 0 of the first problem
-// of every adapter-product launch withholds the loads of its first stage, so
-// that its MMA thread's bounded wait runs out and the launch takes its
-// timeout path (status bit, early exit, TMEM released).
-__device__ int g_qlora_inject_stall = 0;
-
 template <int A_MN, int B_MN>
 __global__ void __launch_bounds__(kSkThreads, 1)
     k_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
@@ -252,7 +246,7 @@ __global__ void __launch_bounds__(kSkThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       int issued = 0;
-      const bool stall = bid == 0 && !second && *reinterpret_cast<volatile int*>(&g_qlora_inject_stall) != 0;
+      const bool stall = bid == 0 && !second && qlora_stalled();
       for (int it = 0; it < nch; ++it) {
         const int s = it % S;
         if (it >= S && !mbar_wait(smem_u32(&empty[s]), ((it / S) + 1) & 1, abort_flag, args.status)) break;

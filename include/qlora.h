@@ -412,7 +412,7 @@ qlora_status qlora_fp8_linear_bwd(const void* dY, qlora_dtype dy_dtype, int64_t 
  * X, Y: `dtype` (fp32 or bf16), ldx / ldy elements between rows; weight,
  * bias [cols]: w_dtype, either may be NULL (ones, zeros).  mean, rstd: fp32
  * [rows], each written when non-NULL, for the backward.  Y may be X (same
- * stride), otherwise they may not overlap.  eps >= 0, finite.  rows = 0 is
+ * stride, refused otherwise); apart from that they may not overlap.  eps >= 0, finite.  rows = 0 is
  * a no-op.  Pointers aligned to their element.
  *
  * Backward, from the saved mean and rstd:
@@ -421,7 +421,7 @@ qlora_status qlora_fp8_linear_bwd(const void* dY, qlora_dtype dy_dtype, int64_t 
  *     dweight = sum over rows of dy * xh;  dbias = sum over rows of dy
  * dweight, dbias [cols]: grad_dtype, overwritten, each skipped when NULL
  * (a frozen norm passes both NULL and needs no workspace); with rows = 0
- * they are zeros.  dX may be dY or X (same stride).  Workspace (16-byte
+ * they are zeros.  dX may be dY or X (same stride, refused otherwise).  Workspace (16-byte
  * aligned): qlora_layernorm_workspace_bytes(rows, cols), 0 for an invalid
  * shape or none needed.  Sums and statistics are fp32, outputs are rounded
  * once; results are deterministic (fixed summation order, no atomics).
@@ -484,8 +484,9 @@ qlora_status qlora_distill_topk_bwd(const void* Z, int64_t ldz, int64_t rows, in
  *   qlora_debug_set_wait_limit: the bound in ns for the current device
  *     (0 restores 2 s); a synchronous copy to device memory.
  *   qlora_debug_inject_stall(on): while on, CTA 0 of every adapter-product
- *     launch of this library (the T = X A^T, G = dY B and dA/dB products)
- *     withholds the loads of its first pipeline stage, so that its wait
+ *     launch of this library (the T = X A^T, G = dY B and dA/dB products),
+ *     of every FP8 product of many tokens and of every layer norm of many
+ *     rows withholds the loads of its first pipeline stage, so that its wait
  *     runs out; the launch then ends early with the timeout bit set and the
  *     call's outputs unspecified.  Calls after it is switched off are
  *     unaffected (each call clears the arrival counters it uses).

@@ -96,17 +96,19 @@ def test_layernorm_refusals():
     for i, v in ((0, None), (0, FAKE + 1), (1, 63), (2, -1), (3, 0), (4, 5), (7, 5), (8, -1.0), (8, float("nan")),
                  (9, None), (9, FAKE + 1), (10, 63), (5, FAKE + 1), (6, FAKE + 1), (11, FAKE + 2), (12, FAKE + 2)):
         assert f(i, v) == INVALID, (i, v)
+    assert L.qlora_layernorm_fwd(FAKE, 64, 4, 64, 1, None, None, 1, 1e-5, FAKE, 72, None, None, None, None) == INVALID
     need = q.qlora_layernorm_workspace_bytes(4, 64)
     assert need > 0 and q.qlora_layernorm_workspace_bytes(0, 64) == 0
     assert q.qlora_layernorm_workspace_bytes(-1, 64) == 0 and q.qlora_layernorm_workspace_bytes(4, 0) == 0
-    bwd = [FAKE, 64, FAKE, 64, 4, 64, 1, FAKE, 1, FAKE, FAKE, FAKE, 64, FAKE, FAKE, 0, FAKE, need, None, None]
+    other = FAKE + 4096
+    bwd = [FAKE, 64, other, 64, 4, 64, 1, FAKE, 1, FAKE, FAKE, FAKE, 64, FAKE, FAKE, 0, FAKE, need, None, None]
 
     def b(i, v):
         a = list(bwd)
         a[i] = v
         return L.qlora_layernorm_bwd(*a)
     for i, v in ((0, None), (2, None), (9, None), (10, None), (11, None), (1, 60), (3, 60), (12, 60), (4, -2), (5, 0),
-                 (6, 9), (8, 9), (15, 9), (13, FAKE + 2), (14, FAKE + 2), (11, FAKE + 1)):
+                 (6, 9), (8, 9), (15, 9), (13, FAKE + 2), (14, FAKE + 2), (11, FAKE + 1), (12, 72)):   # in place, another stride
         assert b(i, v) == INVALID, (i, v)
     assert b(16, None) == WORKSPACE and b(16, FAKE + 8) == WORKSPACE and b(17, need - 1) == WORKSPACE
 
