@@ -413,7 +413,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 constexpr int kLnMaxStages = 8;
 // After a wait that gave up: the loads still under way land before the block
 // can exit (bounded).  By the thread that asked for them.
-__device__ __forceinline__ void ln_drain(uint64_t* full, int stages, int64_t asked) {
+__device__ __noinline__ void ln_drain(uint64_t* full, int stages, int64_t asked) {
   for (int64_t i = asked > stages ? asked - stages : 0; i < asked; ++i) {
     const uint64_t t0 = global_ns();
     while (!mbar_try_wait(smem_u32(&full[i % stages]), static_cast<uint32_t>((i / stages) & 1)) &&
@@ -460,26 +460,30 @@ __global__ void __launch_bounds__(GROUP, 1024 / GROUP) k_ln_fwd_ring(const LnArg
   __shared__ __align__(16) float2 red[2][32];
   __shared__ uint64_t full[kLnMaxStages];
   __shared__ int abort_word;
+  __shared__ int asked;                    // rows asked for (thread 0's; kept out of its registers)
   const int t = threadIdx.x;
   const int cols = static_cast<int>(a.cols);
   const uint32_t row_bytes = static_cast<uint32_t>(cols * sizeof(T));
-  const int64_t mine = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;   // rows of this block
+  const int mine = static_cast<int>((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);   // rows of this block
   if (t == 0) {
     for (int i = 0; i < a.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
     abort_word = 0;
+    asked = 0;
     fence_mbar_init();
   }
   __syncthreads();
-  auto ask = [&](int64_t i, int s) {       // row i of this block into slot s
+  auto ask = [&](int i, int s) {       // row i of this block into slot s
+    asked = i + 1;
     mbar_arrive_expect_tx(smem_u32(&full[s]), row_bytes);
-    if (i == 0 && blockIdx.x == 0 && qlora_stalled()) return;   // the test hook: this row never comes
-    bulk_load(smem_u32(ring) + s * row_bytes, static_cast<const T*>(a.x) + (blockIdx.x + i * gridDim.x) * a.ldx, row_bytes,
+    bulk_load(smem_u32(ring) + s * row_bytes, static_cast<const T*>(a.x) + static_cast<int64_t>(blockIdx.x + i * gridDim.x) * a.ldx, row_bytes,
               smem_u32(&full[s]));
   };
-  int64_t asked = 0;                       // rows asked for, by thread 0
-  bool came = true;                        // every row so far
-  if (t == 0)
-    for (; asked < a.stages && asked < mine; ++asked) ask(asked, static_cast<int>(asked));
+  if (t == 0) {
+    // (the test hook: the first row never comes, its barrier only expects it)
+    const bool stall = blockIdx.x == 0 && qlora_stalled();
+    if (stall) mbar_arrive_expect_tx(smem_u32(&full[0]), row_bytes);
+    for (int i = stall ? 1 : 0; i < a.stages && i < mine; ++i) ask(i, i);
+  }
   f32x2 w[PER][H], b[PER][H];
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
@@ -492,8 +496,9 @@ __global__ void __launch_bounds__(GROUP, 1024 / GROUP) k_ln_fwd_ring(const LnArg
   const float inv = 1.0f / static_cast<float>(cols);
   int s = 0;
   uint32_t parity = 0;
-  for (int64_t i = 0; i < mine; ++i) {
-    const int64_t row = blockIdx.x + i * gridDim.x;
+  bool came = true;                        // every row so far
+  for (int i = 0; i < mine; ++i) {
+    const int64_t row = static_cast<int>(blockIdx.x + i * gridDim.x);
     // A wait that gives up says so in *status.  Every later wait then gives up
     // at once, and no more rows are asked for (a slot whose row has not come
     // is still in its old phase), so the launch runs out quickly.
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(GROUP, 1024 / GROUP) k_ln_fwd_ring(const LnArg
     }
     float2 sum = unpair2(acc);
     const float mean = ln_group_sum1<GROUP>(sum.x + sum.y, red[0]) * inv;
-    if (t == 0 && came && asked < mine) ask(asked++, s);
+    if (t == 0 && i + a.stages < mine && came) ask(i + a.stages, s);
     const f32x2 neg = pair2(-mean, -mean);
     acc = 0;
 #pragma unroll
@@ -551,28 +556,32 @@ __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
   __shared__ __align__(16) float2 red[2][32];
   __shared__ uint64_t full[kLnMaxStages];
   __shared__ int abort_word;
+  __shared__ int asked;                    // rows asked for (thread 0's; kept out of its registers)
   const int t = threadIdx.x;
   const int cols = static_cast<int>(a.cols);
   const uint32_t row_bytes = static_cast<uint32_t>(cols * sizeof(T));
-  const int64_t mine = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
+  const int mine = static_cast<int>((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
   if (t == 0) {
     for (int i = 0; i < a.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
     abort_word = 0;
+    asked = 0;
     fence_mbar_init();
   }
   __syncthreads();
-  auto ask = [&](int64_t i, int s) {       // rows i of x and dy into slot s
-    const int64_t row = blockIdx.x + i * gridDim.x;
+  auto ask = [&](int i, int s) {       // rows i of x and dy into slot s
+    asked = i + 1;
+    const int64_t row = static_cast<int>(blockIdx.x + i * gridDim.x);
     const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(ring) + 2 * s * row_bytes;
     mbar_arrive_expect_tx(bar, 2 * row_bytes);
-    if (i == 0 && blockIdx.x == 0 && qlora_stalled()) return;   // the test hook: these rows never come
     bulk_load(dst, static_cast<const T*>(a.x) + row * a.ldx, row_bytes, bar);
     bulk_load(dst + row_bytes, static_cast<const T*>(a.dy) + row * a.lddy, row_bytes, bar);
   };
-  int64_t asked = 0;                       // rows asked for, by thread 0
-  bool came = true;                        // every row so far
-  if (t == 0)
-    for (; asked < a.stages && asked < mine; ++asked) ask(asked, static_cast<int>(asked));
+  if (t == 0) {
+    // (the test hook: the first row never comes, its barrier only expects it)
+    const bool stall = blockIdx.x == 0 && qlora_stalled();
+    if (stall) mbar_arrive_expect_tx(smem_u32(&full[0]), row_bytes);
+    for (int i = stall ? 1 : 0; i < a.stages && i < mine; ++i) ask(i, i);
+  }
   f32x2 w[PER][H], dw[PER][H], db[PER][H];
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
@@ -584,9 +593,10 @@ __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
   const float inv = 1.0f / static_cast<float>(cols);
   int s = 0;
   uint32_t parity = 0;
+  bool came = true;                        // every row so far
   float mu = a.mean[blockIdx.x], rs = a.rstd[blockIdx.x];
-  for (int64_t i = 0; i < mine; ++i) {
-    const int64_t row = blockIdx.x + i * gridDim.x;
+  for (int i = 0; i < mine; ++i) {
+    const int64_t row = static_cast<int>(blockIdx.x + i * gridDim.x);
     const int64_t next = i + 1 < mine ? row + gridDim.x : row;
     const float mu_next = a.mean[next], rs_next = a.rstd[next];
     came = mbar_wait(smem_u32(&full[s]), parity, &abort_word, a.status) && came;   // (as in the forward)
@@ -612,7 +622,7 @@ __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
     }
     const float2 p = unpair2(sg), q = unpair2(sgx);
     const float2 sum = ln_group_sum<GROUP>(make_float2(p.x + p.y, q.x + q.y), red[i & 1]);
-    if (t == 0 && came && asked < mine) ask(asked++, s);
+    if (t == 0 && i + a.stages < mine && came) ask(i + a.stages, s);
     const float m1 = -sum.x * inv, m2 = -sum.y * inv;
     const f32x2 n1 = pair2(m1, m1), n2 = pair2(m2, m2);
     T* dx = static_cast<T*>(a.dx) + row * a.lddx;
