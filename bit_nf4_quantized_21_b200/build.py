@@ -1,5 +1,6 @@
-"""Build libqlora.so in-tree for sm_100a with nvcc, and its debug build
-libqlora_debug.so (-DQLORA_DEBUG_CHECKS: index-range checks in the kernels).
+"""Build libqlora.so in-tree for sm_100a with nvcc, its debug build
+libqlora_debug.so (-DQLORA_DEBUG_CHECKS: index-range checks in the kernels),
+and with g++ the compiled part of the Python binding, _calls.so.
 
     python -m bit_nf4_quantized_21_b200.build        # rebuild when sources changed
     python -m bit_nf4_quantized_21_b200.build -v     # also print ptxas resource usage
@@ -10,6 +11,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqlora.so")
 LIB_DEBUG = os.path.join(PKG, "libqlora_debug.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -40,6 +43,7 @@ def needs_build(lib: str = LIB) -> bool:
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     lib = LIB_DEBUG if debug else LIB
+    build_calls(force)
     if not force and not needs_build(lib) and not verbose:
         return lib
     nvcc = os.environ.get("NVCC", "nvcc")
@@ -51,6 +55,26 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     subprocess.run(cmd, check=True)
     os.replace(tmp, lib)
     return lib
+
+
+def build_calls(force: bool = False) -> str:
+    """_calls.so: host code against the headers and libraries of the installed torch."""
+    sources = [os.path.join(CSRC, "calls.cpp"), os.path.join(INCLUDE, "qlora.h")]
+    if not force and os.path.exists(CALLS) and all(os.path.getmtime(s) <= os.path.getmtime(CALLS) for s in sources):
+        return CALLS
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME") or "/usr/local/cuda"
+    include = [INCLUDE, os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include/torch/csrc/api/include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = CALLS + f".{os.getpid()}.tmp"
+    # the compiler that nvcc uses too: one that links libstdc++ statically would put a second copy beside torch's
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wno-attributes",
+                    *(f for d in include for f in ("-isystem", d)), "-o", tmp, sources[0],
+                    "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ldl"],
+                   check=True)
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 if __name__ == "__main__":

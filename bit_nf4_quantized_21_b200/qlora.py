@@ -1,16 +1,15 @@
-"""Python binding of libqlora (ctypes): argument marshalling only.
+"""Python binding of libqlora: argument marshalling only (ctypes, and for the
+FP8 layer, the layer norm and the distillation loss the compiled _calls).
 
 Every function here has the name of the C entry point it calls
 (include/qlora.h) and does nothing but turn torch tensors into device
 pointers, pick up the current CUDA stream, call the library and raise on a
-non-OK status.  There is no fallback path: if libqlora.so is missing, or a
+non-OK status.  There is no fallback path: if libqlora.so (or _calls.so) is missing, or a
 tensor is not on a CUDA device, the call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -83,6 +82,7 @@ class FP8MatrixC(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_calls_mod = None
 
 
 def lib() -> ctypes.CDLL:
@@ -525,68 +525,41 @@ def qlora_paged_prefetch(ptr: int, nbytes: int, to_device: bool = True, stream=N
            "qlora_paged_prefetch")
 
 
-# --------------------------------------- strided operands of the calls below
+# ------------------- FP8 layer, layer norm, distillation: calls of module _calls
+#
+# These serve single tokens too, where a kernel takes a few microseconds: the
+# marshalling is compiled (csrc/calls.cpp).  Their tensors may be rows of
+# wider matrices (rows contiguous, any distance apart); all of a call's tensors
+# are on one device, which need not be the current one.
 
-_DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
-
-
-def _dtype(t: torch.Tensor, name: str) -> int:
-    d = _DTYPES.get(t.dtype)
-    if d is None:
-        raise ValueError(f"{name} must be fp32 or bf16")
-    return d
-
-
-# These calls serve single tokens, where a launch takes a few microseconds: the
-# checks below read each property of a tensor once.
-
-def _matrix(t: torch.Tensor, name: str, rows: int | None = None, cols: int | None = None) -> tuple[int, int]:
-    """(pointer, elements between rows) of a 2-D tensor whose rows are contiguous."""
-    shape = t.shape
-    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
-        raise ValueError(f"{name} must be 2-D [{'rows' if rows is None else rows}, {'cols' if cols is None else cols}]"
-                         f", got {tuple(shape)}")
-    n, c = shape
-    ld, step = t.stride()
-    if step != 1 and c > 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if n <= 1:
-        ld = c
-    elif ld < c:
-        raise ValueError(f"{name}: rows overlap")
-    return t.data_ptr(), ld
+def _calls():
+    """The compiled marshalling, on the same libqlora build as lib()."""
+    global _calls_mod
+    if _calls_mod is None:
+        lib()
+        try:
+            from . import _calls as m
+        except ImportError as e:
+            raise RuntimeError("the compiled binding _calls.so is missing; build it with "
+                               "`python -m bit_nf4_quantized_21_b200.build`") from e
+        m.init(LIB_PATH)
+        _calls_mod = m
+    return _calls_mod
 
 
-def _vector(t: torch.Tensor | None, name: str, n: int, dtype=None) -> int | None:
-    if t is None:
-        return None
-    if t.numel() != n or (dtype is not None and t.dtype != dtype) or not t.is_contiguous():
-        raise ValueError(f"{name} must have {n} contiguous elements" + (f" of {dtype}" if dtype is not None else ""))
-    return t.data_ptr()
+def _status(r, where: str):
+    if r.__class__ is int:
+        _check(r, where)
+    return r
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _on(stream, *tensors):
-    """The context of a call: its tensors' one device made current, and its
-    stream, so that what the call allocates belongs to the stream that uses it."""
-    dev = tensors[0].get_device()
-    if dev < 0:
+def _stream_of(stream, t: torch.Tensor):
+    """The context that makes `stream` current for a call on t's device."""
+    if not t.is_cuda:
         raise ValueError("libqlora takes CUDA tensors only")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("all tensors of a call must be on one CUDA device")
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError("the stream must belong to the tensors' device")
-        return torch.cuda.stream(stream)
-    return _HERE if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
-
-
-def _current(t: torch.Tensor) -> int:
-    """The current stream of t's device (current_stream() without its Stream object)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    if stream.device != t.device:
+        raise ValueError("the stream must belong to the tensors' device")
+    return torch.cuda.stream(stream)
 
 
 # ------------------------------------------------------------- FP8 linear layer
@@ -600,26 +573,8 @@ class FP8Matrix:
     codes: torch.Tensor                 # uint8 (or float8_e4m3fn) [rows, ld]
     scale: torch.Tensor                 # fp32 [ceil(rows/128), ceil(cols/128)], or [ceil(cols/128), rows]
 
-    def c(self) -> FP8MatrixC:
-        if self.codes.element_size() != 1 or self.scale.dtype != torch.float32:
-            raise ValueError("codes are bytes and scales fp32")
-        p, ld = _matrix(self.codes, "codes", self.rows)
-        if self.codes.shape[1] < -(-self.cols // 16) * 16:
-            raise ValueError("codes: a row holds cols rounded up to 16 bytes")
-        want = -(-self.rows // self.block_rows) * -(-self.cols // 128) if self.block_rows in (1, 128) else -1
-        return FP8MatrixC(self.rows, self.cols, ld, self.block_rows, 0, p, _vector(self.scale, "scale", want))
-
     def nbytes(self) -> int:
         return self.codes.numel() + 4 * self.scale.numel()
-
-
-def _fp8_scratch(X: torch.Tensor, rows: int, cols: int):
-    """(descriptor, owner) of quantised activations [rows, cols] that live for one call."""
-    kb = -(-cols // 128)
-    codes = rows * kb * 128
-    buf = X.new_empty(codes + 4 * kb * rows, dtype=torch.uint8)
-    p = buf.data_ptr()
-    return FP8MatrixC(rows, cols, kb * 128, 1, 0, p, p + codes), buf
 
 
 def qlora_fp8_sizes(rows: int, cols: int, block_rows: int = 128) -> tuple[int, int]:
@@ -638,47 +593,30 @@ def empty_fp8(rows: int, cols: int, device, block_rows: int = 128) -> FP8Matrix:
 
 def qlora_fp8_quantize(X: torch.Tensor, out: FP8Matrix | None = None, block_rows: int = 128,
                        d_status: torch.Tensor | None = None, stream=None) -> FP8Matrix:
-    """E4M3 codes and scales of X: block_rows = 128 for a weight, 1 for activations."""
-    dt = _dtype(X, "X")
-    if block_rows not in (1, 128):
-        raise ValueError("block_rows is 1 or 128")
-    with _on(stream, X, d_status, *(() if out is None else (out.codes, out.scale))):
-        if out is None:
-            out = empty_fp8(X.shape[0], X.shape[1], X.device, block_rows)
-        p, ld = _matrix(X, "X", out.rows, out.cols)
-        _check(lib().qlora_fp8_quantize(p, dt, ld, ctypes.byref(out.c()), _ptr(d_status), _current(X)),
-               "qlora_fp8_quantize")
+    """E4M3 codes and scales of X (fp32 or bf16): block_rows = 128 for a weight, 1 for activations."""
+    if stream is not None:
+        with _stream_of(stream, X):
+            return qlora_fp8_quantize(X, out, block_rows, d_status)
+    if block_rows not in (1, 128) or X.dim() != 2:
+        raise ValueError("X must be 2-D and block_rows 1 or 128")
+    if out is None:
+        out = empty_fp8(X.shape[0], X.shape[1], X.device, block_rows)
+    _status(_calls().fp8_quantize(X, out.rows, out.cols, out.block_rows, out.codes, out.scale, d_status),
+            "qlora_fp8_quantize")
     return out
 
 
-def _fp8_linear(where, X, Wq, out, out_dtype, Xq, d_status, stream, in_cols, out_cols):
-    quantised = isinstance(X, FP8Matrix)
-    with _on(stream, Wq.codes, Wq.scale, out, d_status, *((X.codes, X.scale) if quantised else (X,)),
-             *(() if Xq is None else (Xq.codes, Xq.scale))):
-        keep = None
-        if quantised:
-            if Xq is not None:
-                raise ValueError("already quantised activations need no scratch")
-            p, dt, ld, rows, cx = None, QLORA_F32, 0, X.rows, X.c()
-        else:
-            p, ld = _matrix(X, "activations", cols=in_cols)
-            dt = _dtype(X, "activations")
-            rows = X.shape[0]
-            if Xq is None:
-                cx, keep = _fp8_scratch(X, rows, in_cols)
-            elif Xq.rows != rows:
-                raise ValueError("the scratch must have the activations' rows")
-            else:
-                cx = Xq.c()
-        if out is None:
-            out = Wq.codes.new_empty((rows, out_cols), dtype=out_dtype)
-            o, ldo = out.data_ptr(), out_cols
-        else:
-            o, ldo = _matrix(out, "output", rows, out_cols)
-        _check(getattr(lib(), where)(p, dt, ld, ctypes.byref(Wq.c()), ctypes.byref(cx), o, _dtype(out, "output"), ldo,
-                                     _ptr(d_status), _current(out)), where)
-        del keep                        # (its memory is reused on this stream only)
-    return out
+def _fp8_linear(where, bwd, X, W, out, out_dtype, q, d_status, stream):
+    if stream is not None:
+        with _stream_of(stream, W.codes):
+            return _fp8_linear(where, bwd, X, W, out, out_dtype, q, d_status, None)
+    if isinstance(X, FP8Matrix):
+        if q is not None:
+            raise ValueError("already quantised activations need no scratch")
+        X, q = None, X
+    xq = (None, None, None, None, None) if q is None else (q.rows, q.cols, q.block_rows, q.codes, q.scale)
+    return _status((_calls_mod or _calls()).fp8_linear(bwd, X, *xq, W.rows, W.cols, W.block_rows, W.codes, W.scale, out,
+                                                       out_dtype, d_status), where)
 
 
 def qlora_fp8_linear_fwd(X: torch.Tensor | FP8Matrix, Wq: FP8Matrix, Y: torch.Tensor | None = None,
@@ -686,54 +624,31 @@ def qlora_fp8_linear_fwd(X: torch.Tensor | FP8Matrix, Wq: FP8Matrix, Y: torch.Te
                          d_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = Q(X) W^T.  X: fp32 or bf16 [M, K], or an FP8Matrix (block_rows = 1) of them; Xq: where the
     quantised X goes (allocated when not given)."""
-    return _fp8_linear("qlora_fp8_linear_fwd", X, Wq, Y, out_dtype, Xq, d_status, stream, Wq.cols, Wq.rows)
+    return _fp8_linear("qlora_fp8_linear_fwd", False, X, Wq, Y, out_dtype, Xq, d_status, stream)
 
 
 def qlora_fp8_linear_bwd(dY: torch.Tensor | FP8Matrix, Wq: FP8Matrix, dX: torch.Tensor | None = None,
                          out_dtype=torch.bfloat16, dYq: FP8Matrix | None = None,
                          d_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dX = Q(dY) W for dY [M, N]; the frozen weight has no gradient."""
-    return _fp8_linear("qlora_fp8_linear_bwd", dY, Wq, dX, out_dtype, dYq, d_status, stream, Wq.rows, Wq.cols)
+    return _fp8_linear("qlora_fp8_linear_bwd", True, dY, Wq, dX, out_dtype, dYq, d_status, stream)
 
 
 # ------------------------------------------------------------------- layer norm
 
-@functools.lru_cache(maxsize=256)
 def qlora_layernorm_workspace_bytes(rows: int, cols: int) -> int:
     return int(lib().qlora_layernorm_workspace_bytes(rows, cols))
-
-
-def _param(p: torch.Tensor | None, cols: int) -> int | None:
-    return None if p is None else _vector(p, "weight and bias", cols)
 
 
 def qlora_layernorm_fwd(X: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                         eps: float = 1e-5, Y: torch.Tensor | None = None, mean: torch.Tensor | None = None,
                         rstd: torch.Tensor | None = None, d_status: torch.Tensor | None = None, stream=None):
     """(Y, mean, rstd) of the rows of X [rows, cols]; mean and rstd (fp32 [rows]) are what the backward needs."""
-    with _on(stream, X, weight, bias, Y, mean, rstd, d_status):
-        x, ldx = _matrix(X, "X")
-        rows, cols = X.shape
-        like = weight if weight is not None else bias
-        if weight is not None and bias is not None and weight.dtype != bias.dtype:
-            raise ValueError("weight and bias must have one type")
-        if Y is None:
-            Y = torch.empty_like(X, memory_format=torch.contiguous_format)
-            y, ldy = Y.data_ptr(), cols
-        elif Y.dtype != X.dtype:
-            raise ValueError("Y has X's type")
-        else:
-            y, ldy = _matrix(Y, "Y", rows, cols)
-        if mean is None:
-            mean = X.new_empty(rows, dtype=torch.float32)
-        if rstd is None:
-            rstd = torch.empty_like(mean)
-        _check(lib().qlora_layernorm_fwd(x, ldx, rows, cols, _dtype(X, "X"), _param(weight, cols), _param(bias, cols),
-                                         QLORA_F32 if like is None else _dtype(like, "weight and bias"), eps, y, ldy,
-                                         _vector(mean, "mean", rows, torch.float32),
-                                         _vector(rstd, "rstd", rows, torch.float32), _ptr(d_status), _current(X)),
-               "qlora_layernorm_fwd")
-    return Y, mean, rstd
+    if stream is not None:
+        with _stream_of(stream, X):
+            return qlora_layernorm_fwd(X, weight, bias, eps, Y, mean, rstd, d_status)
+    return _status((_calls_mod or _calls()).layernorm_fwd(X, weight, bias, eps, Y, mean, rstd, d_status),
+                   "qlora_layernorm_fwd")
 
 
 def qlora_layernorm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
@@ -741,61 +656,15 @@ def qlora_layernorm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor 
                         dbias: torch.Tensor | None = None, grad_dtype=torch.float32, want_params: bool = True,
                         workspace: torch.Tensor | None = None, d_status: torch.Tensor | None = None, stream=None):
     """(dX, dweight, dbias); want_params=False for a frozen norm (the two are None, unless given)."""
-    with _on(stream, dY, X, weight, mean, rstd, dX, dweight, dbias, workspace, d_status):
-        x, ldx = _matrix(X, "X")
-        rows, cols = X.shape
-        dy, lddy = _matrix(dY, "dY", rows, cols)
-        if dX is None:
-            dX = torch.empty_like(X, memory_format=torch.contiguous_format)
-            dx, lddx = dX.data_ptr(), cols
-        else:
-            dx, lddx = _matrix(dX, "dX", rows, cols)
-        if dY.dtype != X.dtype or dX.dtype != X.dtype:
-            raise ValueError("dY and dX have X's type")
-        if want_params:
-            gt = dweight.dtype if dweight is not None else dbias.dtype if dbias is not None else grad_dtype
-            if dweight is None:
-                dweight = X.new_empty(cols, dtype=gt)
-            if dbias is None:
-                dbias = torch.empty_like(dweight, dtype=gt)
-        if dweight is not None and dbias is not None and dweight.dtype != dbias.dtype:
-            raise ValueError("dweight and dbias must have one type")
-        grad = dweight if dweight is not None else dbias
-        ws, ws_bytes = None, 0
-        if grad is not None:
-            if workspace is None:
-                ws_bytes = max(qlora_layernorm_workspace_bytes(rows, cols), 16)
-                workspace = X.new_empty(ws_bytes, dtype=torch.uint8)
-                ws = workspace.data_ptr()
-            else:
-                ws, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-        _check(lib().qlora_layernorm_bwd(dy, lddy, x, ldx, rows, cols, _dtype(X, "X"), _param(weight, cols),
-                                         QLORA_F32 if weight is None else _dtype(weight, "weight and bias"),
-                                         _vector(mean, "mean", rows, torch.float32),
-                                         _vector(rstd, "rstd", rows, torch.float32), dx, lddx,
-                                         _vector(dweight, "dweight", cols), _vector(dbias, "dbias", cols),
-                                         QLORA_F32 if grad is None else _dtype(grad, "dweight and dbias"), ws,
-                                         ws_bytes, _ptr(d_status), _current(X)), "qlora_layernorm_bwd")
-    return dX, dweight, dbias
+    if stream is not None:
+        with _stream_of(stream, X):
+            return qlora_layernorm_bwd(dY, X, weight, mean, rstd, dX, dweight, dbias, grad_dtype, want_params, workspace,
+                                       d_status)
+    return _status((_calls_mod or _calls()).layernorm_bwd(dY, X, weight, mean, rstd, dX, dweight, dbias, grad_dtype,
+                                                          want_params, workspace, d_status), "qlora_layernorm_bwd")
 
 
 # ----------------------------------------------------------------- distillation
-
-def _distill(Z, ids, t, row_weight, dZ):
-    z, ldz = _matrix(Z, "Z")
-    rows, vocab = Z.shape
-    if ids.dtype not in (torch.int32, torch.int64):
-        raise ValueError("ids are int32 or int64")
-    if ids.dim() != 2 or ids.shape[0] != rows or t.shape != ids.shape:
-        raise ValueError("ids and t must be [rows, top]")
-    if dZ is not None and dZ.dtype != Z.dtype:
-        raise ValueError("dZ has Z's type")
-    d, lddz = (None, 0) if dZ is None else _matrix(dZ, "dZ", rows, vocab)
-    if dZ is not None and rows == 1 and d == z:
-        lddz = ldz
-    return ((z, ldz, rows, vocab, _dtype(Z, "Z"), _ptr(ids), 32 if ids.dtype == torch.int32 else 64, _ptr(t),
-             _dtype(t, "t"), ids.shape[1]), _vector(row_weight, "row_weight", rows, torch.float32), (d, lddz))
-
 
 def qlora_distill_topk_fwd(Z: torch.Tensor, ids: torch.Tensor, t: torch.Tensor, tau: float = 1.0,
                            row_weight: torch.Tensor | None = None, loss: torch.Tensor | None = None,
@@ -804,17 +673,11 @@ def qlora_distill_topk_fwd(Z: torch.Tensor, ids: torch.Tensor, t: torch.Tensor, 
     """(loss, lse), fp32 [rows], of student logits Z [rows, vocab] against a teacher's top logits t at ids
     [rows, top] (negative ids: unused places).  With dZ (Z itself, or a tensor like it) the same launch
     writes the gradient of the sum of the losses."""
-    with _on(stream, Z, ids, t, row_weight, loss, lse, dZ, d_status):
-        args, w, d = _distill(Z, ids, t, row_weight, dZ)
-        rows = Z.shape[0]
-        if loss is None:
-            loss = Z.new_empty(rows, dtype=torch.float32)
-        if lse is None:
-            lse = torch.empty_like(loss)
-        _check(lib().qlora_distill_topk_fwd(*args, float(tau), w, _vector(loss, "loss", rows, torch.float32),
-                                            _vector(lse, "lse", rows, torch.float32), *d, _ptr(d_status), _current(Z)),
-               "qlora_distill_topk_fwd")
-    return loss, lse
+    if stream is not None:
+        with _stream_of(stream, Z):
+            return qlora_distill_topk_fwd(Z, ids, t, tau, row_weight, loss, lse, dZ, d_status)
+    return _status((_calls_mod or _calls()).distill_fwd(Z, ids, t, tau, row_weight, loss, lse, dZ, d_status),
+                   "qlora_distill_topk_fwd")
 
 
 def qlora_distill_topk_bwd(Z: torch.Tensor, ids: torch.Tensor, t: torch.Tensor, tau: float, lse: torch.Tensor,
@@ -822,12 +685,8 @@ def qlora_distill_topk_bwd(Z: torch.Tensor, ids: torch.Tensor, t: torch.Tensor, 
                            dZ: torch.Tensor | None = None, d_status: torch.Tensor | None = None,
                            stream=None) -> torch.Tensor:
     """The gradient of the losses (weighted by grad_loss) with respect to Z, from the forward's lse."""
-    with _on(stream, Z, ids, t, row_weight, lse, grad_loss, dZ, d_status):
-        if dZ is None:
-            dZ = torch.empty_like(Z, memory_format=torch.contiguous_format)
-        args, w, d = _distill(Z, ids, t, row_weight, dZ)
-        rows = Z.shape[0]
-        _check(lib().qlora_distill_topk_bwd(*args, float(tau), w, _vector(lse, "lse", rows, torch.float32),
-                                            _vector(grad_loss, "grad_loss", rows, torch.float32), *d, _ptr(d_status),
-                                            _current(Z)), "qlora_distill_topk_bwd")
-    return dZ
+    if stream is not None:
+        with _stream_of(stream, Z):
+            return qlora_distill_topk_bwd(Z, ids, t, tau, lse, row_weight, grad_loss, dZ, d_status)
+    return _status((_calls_mod or _calls()).distill_bwd(Z, ids, t, tau, lse, row_weight, grad_loss, dZ, d_status),
+                   "qlora_distill_topk_bwd")
