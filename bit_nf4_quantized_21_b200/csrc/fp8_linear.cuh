@@ -11,24 +11,32 @@
 // Products of E4M3 values are exact in the tensor core's fp32 accumulator;
 // each block's sum is scaled and added in fp32; the output is rounded once.
 //
-// k_fp8_gemm (many tokens), tensor bound.  A pair of SMs (tcgen05.mma
-// cta_group::2, kind::f8f6f4) owns a 256 x 256 output tile; each CTA brings
-// its 128 activation rows and its 128-row half of the weight tile by TMA, 32
-// KB per block of 128 in a ring of six.  A block's product cannot stay in the
-// tensor core's accumulator (the scales differ from block to block): it goes
-// into tensor memory, and eight warps take it out and add it to fp32 sums in
+// k_fp8_gemm (many tokens).  A pair of SMs (tcgen05.mma cta_group::2,
+// kind::f8f6f4) owns a 256 x 256 output tile; each CTA brings its 128
+// activation rows and its 128-row half of the weight tile by TMA, 32 KB per
+// block of 128 in a ring of six.  A block's product cannot stay in the tensor
+// core's accumulator (the scales differ from block to block): it goes into
+// tensor memory, and eight warps take it out and add it to fp32 sums in
 // registers, acc = fma(D, sx sw, acc), packed in pairs; a thread holds 128
 // outputs of one row, inside one scale block of the weight.  Tensor memory
-// holds two such products and no more, so what bounds the kernel is how fast
-// a place is free again: commit, wake the epilogue, load, tell the leader,
-// issue.  Hence four accumulators of 128 columns instead of two of 256 (a
-// place waits for half as much work), an issuing thread for each (a thread
-// that waits after issuing MMAs stalls until they drain), and the place is
-// handed back as soon as its values are in registers, before they are used.
-// The grid is one pair per two SMs and walks the tiles, so that a tile's
-// output is written while the next one's products are already running.  The
-// same weight bytes serve both directions: a tile of 128 rows x 128 bytes is
-// a K-major operand forward and an MN-major one in dX.
+// holds two such products and no more, so a place has to be free again soon:
+// four accumulators of 128 columns instead of two of 256 (a place waits for
+// half as much work), an issuing thread for each (a thread that waits after
+// issuing MMAs stalls until they drain), and the place is handed back as soon
+// as its values are in registers, before they are used.  The scales come
+// through shared memory, two blocks ahead (one block ahead, their way was
+// what every block waited for: 2048 x 11008 x 4096 took 99 us).  The grid is
+// one pair per two SMs and walks the tiles, so that a tile's output is written
+// while the next one's products are already running.  The same weight bytes
+// serve both directions: a tile of 128 rows x 128 bytes is a K-major operand
+// forward and an MN-major one in dX.  Where there are few tiles they are 128
+// columns wide, a whole block to an accumulator, three in flight.
+//   Measured with the quantiser ahead of it: 2048 x 11008 x 4096 forward 91
+// us (2.02 PFLOP/s), dX 99 us; 1000 x 4100 x 4040 27 us; 64 x 4096 x 4096 16
+// us.  What bounds it now is the epilogue warps' way for a half of a block:
+// notice that it is there, take 64 columns out (one warp in a quarter of the
+// tensor memory at a time), hand the place back, 32 packed multiply-adds;
+// 0.24 us, where the MMAs need 0.14.
 //
 // k_fp8_gemv (few tokens, forward), HBM bound: the weight streams once from
 // global memory straight into the registers of legacy warp-level MMAs
@@ -388,31 +396,43 @@ __global__ void __launch_bounds__(kF8GemvThreads, 1) k_fp8_gemv(const Fp8GemvArg
 }
 
 // ---------------------------------------------- many tokens: the 2-SM GEMM
-constexpr int kF8Ring = 6;
 constexpr int kF8EpiWarps = 8;
 constexpr int kF8ProdWarp = 8;
-constexpr int kF8IssueWarp = 9;                  // .. 12: four issuers, one per accumulator
+constexpr int kF8IssueWarp = 9;                  // .. 12: an issuer per accumulator
 constexpr int kF8ScaleWarp = 13;
-constexpr int kF8Accs = 4;
+constexpr int kF8ActWarp = 14;
 constexpr int kF8Threads = 32 * 16;
 // registers per thread: what the launch gives everyone, then the epilogue's
 // two warpgroups take what the two others hand back
-constexpr int kF8Regs = 128, kF8EpiRegs = 216, kF8RoleRegs = 40;
+constexpr int kF8Regs = 128, kF8EpiRegs = 208, kF8RoleRegs = 48;
 static_assert(256 * kF8EpiRegs + 256 * kF8RoleRegs <= kF8Threads * kF8Regs, "register split");
 constexpr uint32_t kF8OpBytes = 128 * 128;       // 16 KB: 128 rows x 128 bytes
-constexpr uint32_t kF8SlotBytes = 2 * kF8OpBytes;
 constexpr uint32_t kF8StageBytes = 4096;         // per epilogue warp: 32 rows x 128 bytes of output
-constexpr uint32_t kF8OffStage = kF8Ring * kF8SlotBytes;
-constexpr int kF8ScaleRing = 3;
 constexpr uint32_t kF8ScaleBytes = (128 + 4) * 4; // 128 row scales, the weight's two (and padding)
-constexpr uint32_t kF8OffScale = kF8OffStage + kF8EpiWarps * kF8StageBytes;
-constexpr uint32_t kF8OffBar = kF8OffScale + kF8ScaleRing * kF8ScaleBytes;
-static_assert(kF8OffBar % 8 == 0, "barriers");
-constexpr uint32_t kF8SmemBytes = kF8OffBar + 1024 /*align*/ + 256 /*bars*/;
+// What depends on a tile's width, 128 HALVES columns: a block's product takes
+// HALVES accumulators.
+template <int MODE, int HALVES>
+struct F8Cfg {
+  // (dX takes whole boxes of 128 columns, the swizzle's width, also for its narrow tiles)
+  static constexpr uint32_t kWBytes = MODE == 0 ? kF8OpBytes / 2 * HALVES : kF8OpBytes;
+  static constexpr uint32_t kSlotBytes = kF8OpBytes + kWBytes;
+  static constexpr int kRing = 6;
+  static constexpr int kAccs = HALVES == 2 ? 4 : 3;
+  static constexpr uint32_t kInFlight = kAccs / HALVES;         // blocks that the accumulators hold
+  static constexpr uint32_t kScaleLag = 2;
+  static constexpr uint32_t kScaleRing = kInFlight + kScaleLag;
+  static constexpr uint32_t kOffStage = kRing * kSlotBytes;
+  static constexpr uint32_t kOffScale = kOffStage + kF8EpiWarps * kF8StageBytes;
+  static constexpr uint32_t kOffBar = kOffScale + kScaleRing * kF8ScaleBytes;
+  static constexpr uint32_t kSmem = kOffBar + 256 /*bars*/;
+  static_assert(kOffBar % 8 == 0, "barriers");
+  // An issuer takes every kInFlight-th block and waits for a slot by the
+  // parity of its phase: it must be the one that waited for the phase before.
+  static_assert(kRing % kInFlight == 0, "an issuer comes back to its own slots");
+  static_assert(kSmem <= 227 * 1024, "fp8 GEMM shared memory");
+};
 constexpr uint32_t kF8TmemCols = 512;
 constexpr int kF8GroupM = 8;
-static_assert(kF8Ring % 2 == 0, "an issuer takes every second slot");
-static_assert(kF8SmemBytes <= 227 * 1024, "fp8 GEMM shared memory");
 
 struct Fp8GemmArgs {
   int64_t M;             // activation rows
@@ -464,6 +484,15 @@ __device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint32_t d0, uint32_t d
       : "r"(d0), "r"(d1), "l"(s2));
 }
 
+// four bytes from global to shared memory without passing a register (zero
+// where `in` does not hold; the address is not read then)
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+// one of the arrivals that a barrier counts, once this thread's copies have landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 // whether a phase is complete, without waiting
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -493,20 +522,27 @@ __device__ __forceinline__ void f8_tile(int t, const Fp8GemmArgs& a, int& tm, in
 }
 
 // MODE 0: forward (weight tile K-major), 1: dX (weight tile MN-major)
-template <int MODE>
+template <int MODE, int HALVES>
 __global__ void __launch_bounds__(kF8Threads, 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap tm_act, const __grid_constant__ CUtensorMap tm_w,
                const __grid_constant__ CUtensorMap tm_out, const Fp8GemmArgs args) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kF8OffBar);
+  using C = F8Cfg<MODE, HALVES>;
+  constexpr uint32_t kDepth = C::kInFlight;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = smem_raw;
+  if (smem_u32(base) % 1024 != 0) {      // the swizzled tiles' alignment (no room to round up)
+    if (threadIdx.x == 0 && args.status) atomicOr(args.status, QLORA_DEV_TIMEOUT);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
   uint64_t* full = bars;                         // [ring] leader: both CTAs' tiles landed
-  uint64_t* empty = full + kF8Ring;              // [ring] local: both issuers' MMAs done with the slot
-  uint64_t* acc_full = empty + kF8Ring;          // [4] local: accumulator holds its half of a block's product
-  uint64_t* acc_empty = acc_full + kF8Accs;      // [4] leader: both CTAs have taken it out
-  uint64_t* drained = acc_empty + kF8Accs;       // local: every MMA issued is done
+  uint64_t* empty = full + C::kRing;              // [ring] local: the issuers' MMAs done with the slot
+  uint64_t* acc_full = empty + C::kRing;          // [4] local: accumulator holds its half of a block's product
+  uint64_t* acc_empty = acc_full + C::kAccs;      // [4] leader: both CTAs have taken it out
+  uint64_t* drained = acc_empty + C::kAccs;       // local: every MMA issued is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* act_count = tmem_slot + 2;  // activation tiles asked for
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -518,12 +554,12 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const uint32_t total = static_cast<uint32_t>(mine) * KB;                 // blocks over all of them (host: < 2^31)
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kF8Ring; ++i) { mbar_init(smem_u32(&full[i]), 1); mbar_init(smem_u32(&empty[i]), 2); }
-    for (int i = 0; i < kF8Accs; ++i) {
-      mbar_init(smem_u32(&acc_full[i]), i % 2 == 0 ? 2 : 1);      // the first half also brings the block's scales
+    for (int i = 0; i < C::kRing; ++i) { mbar_init(smem_u32(&full[i]), 1); mbar_init(smem_u32(&empty[i]), HALVES); }
+    for (int i = 0; i < C::kAccs; ++i) {
+      mbar_init(smem_u32(&acc_full[i]), i % HALVES == 0 ? 1 + 32 : 1);   // the first half also brings the block's scales
       mbar_init(smem_u32(&acc_empty[i]), 2 * kF8EpiWarps);
     }
-    mbar_init(smem_u32(drained), kF8Accs);
+    mbar_init(smem_u32(drained), C::kAccs);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -538,112 +574,117 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   tc_fence_after();
   const uint32_t tmem_d = *tmem_slot;
   auto leader_bar = [&](uint64_t* b) { return mapa_shared(smem_u32(b), 0); };
-  if (threadIdx.x == 0) QLORA_CHECK_ONLY(kF8SmemBytes <= dyn_smem_bytes(), 200);
+  if (threadIdx.x == 0) QLORA_CHECK_ONLY(C::kSmem <= dyn_smem_bytes(), 200);
 
   if (warp >= kF8EpiWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RoleRegs));
-    if (warp == kF8ProdWarp && lane == 0) {
-      // ---------------------------------------------------------- producer
+    if (warp == kF8ProdWarp || warp == kF8ActWarp) {
+      // ---------------------------------------------------------- producers
+      // One thread brings the weight's tiles, another the activations' (one
+      // thread for both took 0.37 us per block of a 128-column tile, against
+      // 0.27).
+      const bool weights = warp == kF8ProdWarp;
       uint32_t it = 0;
-      bool live = true;
-      bool waiting = args.after_quant;   // for the activations: they come from the kernel ahead
-      for (int t = pair; t < tiles && live; t += pairs) {
-        int tm, tn;
-        f8_tile(t, args, tm, tn);
-        const int32_t m0 = tm * 256 + static_cast<int32_t>(rank) * 128;
-        const int32_t c0 = tn * 256 + static_cast<int32_t>(rank) * 128;   // this CTA's half of the output columns
-        for (int kb = 0; kb < KB; ++kb, ++it) {
-          const uint32_t s = it % kF8Ring;
-          if (it >= kF8Ring && !mbar_wait(smem_u32(&empty[s]), (it / kF8Ring + 1) & 1, abort_flag, args.status)) {
-            live = false;
-            break;
-          }
-          const uint32_t fb = leader_bar(&full[s]);
-          if (leader) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * kF8SlotBytes);
-          const uint32_t dst = smem_u32(base) + s * kF8SlotBytes;
-          // (a skipped load leaves the slot's wait to run out: bounded, the launch aborts)
-          const bool skip = it == 0 && blockIdx.x == 0 && qlora_stalled();
-          if (!skip && QLORA_CHECK((s + 1) * kF8SlotBytes <= kF8OffStage && m0 >= 0 && c0 >= 0, 201)) {
-            if (MODE == 0) tma_load_2d_pair(dst + kF8OpBytes, &tm_w, fb, kb * kF8Block, c0);
+      if (lane == 0) {
+        bool live = true;
+        if (!weights && args.after_quant) griddep_wait();   // the activations come from the kernel ahead
+        for (int t = pair; t < tiles && live; t += pairs) {
+          int tm, tn;
+          f8_tile(t, args, tm, tn);
+          const int32_t m0 = tm * 256 + static_cast<int32_t>(rank) * 128;
+          const int32_t c0 = (2 * tn + static_cast<int32_t>(rank)) * (64 * HALVES);   // this CTA's half of the output columns
+          for (int kb = 0; kb < KB; ++kb, ++it) {
+            const uint32_t s = it % C::kRing;
+            if (it >= C::kRing && !mbar_wait(smem_u32(&empty[s]), (it / C::kRing + 1) & 1, abort_flag, args.status)) {
+              live = false;
+              break;
+            }
+            const uint32_t fb = leader_bar(&full[s]);
+            if (weights && leader) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * C::kSlotBytes);
+            const uint32_t dst = smem_u32(base) + s * C::kSlotBytes;
+            // (a skipped load leaves the slot's wait to run out: bounded, the launch aborts)
+            if (it == 0 && blockIdx.x == 0 && qlora_stalled()) continue;
+            if (!QLORA_CHECK((s + 1) * C::kSlotBytes <= C::kOffStage && m0 >= 0 && c0 >= 0, 201)) continue;
+            if (!weights) tma_load_2d_pair(dst, &tm_act, fb, kb * kF8Block, m0);
+            else if (MODE == 0) tma_load_2d_pair(dst + kF8OpBytes, &tm_w, fb, kb * kF8Block, c0);
             else tma_load_2d_pair(dst + kF8OpBytes, &tm_w, fb, c0, kb * kF8Block);
           }
-          if (waiting) { griddep_wait(); waiting = false; }
-          if (!skip && QLORA_CHECK((s + 1) * kF8SlotBytes <= kF8OffStage && m0 >= 0, 201))
-            tma_load_2d_pair(dst, &tm_act, fb, kb * kF8Block, m0);
         }
+        if (!weights) *act_count = it;
       }
-      if (*abort_flag && leader) {
+      __syncwarp();
+      named_bar_sync(1, 64);                                // both producers are through
+      if (weights && lane == 0 && *abort_flag && leader) {
         // loads still in flight land before the CTA can exit
-        for (uint32_t i = it > kF8Ring ? it - kF8Ring : 0; i < it; ++i) {
+        it = max(it, *act_count);
+        for (uint32_t i = it > C::kRing ? it - C::kRing : 0; i < it; ++i) {
           const uint64_t t1 = global_ns();
-          while (!mbar_try_wait_cluster(smem_u32(&full[i % kF8Ring]), (i / kF8Ring) & 1) &&
+          while (!mbar_try_wait_cluster(smem_u32(&full[i % C::kRing]), (i / C::kRing) & 1) &&
                  global_ns() - t1 < qlora_drain_limit()) {}
         }
       }
     } else if (warp == kF8ScaleWarp) {
       // ------------------------------------------------------- scale warp
       // The scales of block `it` (128 rows' and the weight's two) into slot
-      // it % 3, two blocks' loads ahead.  The slot is free: block it - 1 has
-      // been computed, so its accumulator was free before, so the epilogue is
-      // through with block it - 3.  Loads in the epilogue's own warps stalled
-      // its multiply-adds (390 cycles for 64 columns against 150).
+      // it % (depth + lag), `lag` blocks ahead, by copies that count towards
+      // the accumulator's barrier when they land (no registers: a value that
+      // is spilled is waited for).  The slot is free: block it - lag has been
+      // computed, so its accumulator was free before, so the epilogue is
+      // through with block it - lag - depth.  Loads in the epilogue's own
+      // warps stalled its multiply-adds (390 cycles for 64 columns against 150).
       const int64_t sw_step = MODE == 0 ? 1 : args.sw_cols, sw_run = MODE == 0 ? args.sw_cols : 1;
       const int64_t runs = (args.out_cols + kF8Block - 1) / kF8Block;
       if (args.after_quant) griddep_wait();
-      uint32_t it = 0;
+      uint32_t it = 0, slot = 0;
       bool live = true;
       for (int t = pair; t < tiles && live; t += pairs) {
         int tm, tn;
         f8_tile(t, args, tm, tn);
         const int64_t row = static_cast<int64_t>(tm) * 256 + rank * 128 + lane;
-        const int64_t ob = 2 * static_cast<int64_t>(tn) + (lane & 1);
-        const float* sa = args.sa + row;
+        const int64_t ob = HALVES == 2 ? 2 * static_cast<int64_t>(tn) + (lane & 1) : tn;
+        const float* sa = args.sa;
         const float* sw = args.sw + (ob < runs ? ob * sw_run : 0);
-        float a[2][4], w[2];
-        auto fetch = [&](int b, int kb) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) a[b][i] = kb < KB && row + 32 * i < args.M ? sa[kb * args.M + 32 * i] : 0.0f;
-          w[b] = kb < KB ? sw[kb * sw_step] : 0.0f;
-        };
-        fetch(0, 0);
-        fetch(1, 1);
-        for (int kb = 0; kb < KB && live; kb += 2) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            if (kb + b >= KB) break;
-            if (it > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&acc_full[2 * ((it - 1) & 1)]), ((it - 1) >> 1) & 1,
-                                                             abort_flag, args.status))) {
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          if (it >= C::kScaleLag) {
+            const uint32_t b = it - C::kScaleLag;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&acc_full[HALVES * (b % kDepth)]), (b / kDepth) & 1, abort_flag,
+                                                   args.status))) {
               live = false;
               break;
             }
-            float* slot = reinterpret_cast<float*>(base + kF8OffScale + (it % kF8ScaleRing) * kF8ScaleBytes);
-            QLORA_CHECK_ONLY(kF8OffScale + (it % kF8ScaleRing + 1) * kF8ScaleBytes <= kF8OffBar, 203);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) slot[lane + 32 * i] = a[b][i];
-            if (lane < 2) slot[128 + lane] = w[b];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&acc_full[2 * (it & 1)]));
-            ++it;
-            fetch(b, kb + b + 2);
           }
+          QLORA_CHECK_ONLY(C::kOffScale + (slot + 1) * kF8ScaleBytes <= C::kOffBar, 203);
+          const uint32_t dst = smem_u32(base) + C::kOffScale + slot * kF8ScaleBytes + 4 * lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool in = row + 32 * i < args.M;
+            cp_async4(dst + 128 * i, in ? sa + row + 32 * i : args.sa, in);
+          }
+          if (lane < 2) cp_async4(dst + 512, sw, true);
+          cp_async_arrive(smem_u32(&acc_full[HALVES * (it % kDepth)]));
+          slot = slot + 1 == C::kScaleRing ? 0 : slot + 1;
+          sa += args.M;
+          sw += sw_step;
         }
       }
-    } else if (warp >= kF8IssueWarp && warp < kF8IssueWarp + kF8Accs && leader) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp >= kF8IssueWarp && warp < kF8IssueWarp + C::kAccs && leader) {
       // --------------------------------------------- MMA issuers (leader)
-      // Issuer j owns accumulator j: half j % 2 of the blocks j / 2, j / 2 +
-      // 2, ...  The half: columns 64 (j % 2) .. of each CTA's 128 weight rows.
+      // Issuer j owns accumulator j: half j % HALVES of the blocks j / HALVES,
+      // j / HALVES + depth, ...  The half: columns 64 (j % HALVES) .. of each
+      // CTA's weight rows.
       // The whole warp runs the loop, so that the descriptors are uniform
       // values; one elected thread issues.
-      const uint32_t j = warp - kF8IssueWarp, half = j & 1;
+      const uint32_t j = warp - kF8IssueWarp, half = j % HALVES;
       constexpr uint32_t idesc = idesc_e4m3(256, 128, MODE);
       const uint32_t dcol = tmem_d + 128u * j;
-      for (uint32_t it = j >> 1; it < total; it += 2) {
-        const uint32_t s = it % kF8Ring, use = it >> 1;
-        bool ok = mbar_wait(smem_u32(&full[s]), (it / kF8Ring) & 1, abort_flag, args.status);
+      for (uint32_t it = j / HALVES; it < total; it += kDepth) {
+        const uint32_t s = it % C::kRing, use = it / kDepth;
+        bool ok = mbar_wait(smem_u32(&full[s]), (it / C::kRing) & 1, abort_flag, args.status);
         ok = ok && (use == 0 || mbar_wait(smem_u32(&acc_empty[j]), (use + 1) & 1, abort_flag, args.status));
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         tc_fence_after();
-        const uint32_t ab = smem_u32(base) + s * kF8SlotBytes, wb = ab + kF8OpBytes + half * (MODE == 0 ? 8192u : 64u);
+        const uint32_t ab = smem_u32(base) + s * C::kSlotBytes, wb = ab + kF8OpBytes + half * (MODE == 0 ? 8192u : 64u);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -662,31 +703,31 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     // ------------------------------------------------------------ epilogue
     // Warp w: rows 32 (w % 4) .. of this CTA; of each accumulator the 64
     // columns that come from CTA p = w / 4's weight rows, so that a warp's
-    // 128 output columns 128 p .. lie in one scale block.
+    // 64 HALVES output columns lie in one scale block.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8EpiRegs));
     const int q = warp & 3, p = warp >> 2;
     const uint32_t taddr = tmem_d + (static_cast<uint32_t>(q * 32) << 16) + 64u * p;
     const uint32_t freed = leader_bar(&acc_empty[0]), filled = smem_u32(&acc_full[0]);
     bool ahead = false;
-    uint8_t* stage = base + kF8OffStage + warp * kF8StageBytes;
+    uint8_t* stage = base + C::kOffStage + warp * kF8StageBytes;
     uint32_t it = 0;
     bool live = true;
     for (int t = pair; t < tiles && live; t += pairs) {
       int tm, tn;
       f8_tile(t, args, tm, tn);
       const int64_t row0 = static_cast<int64_t>(tm) * 256 + rank * 128 + q * 32;
-      const int64_t col = static_cast<int64_t>(tn) * 256 + 128 * p;
-      uint64_t acc[64];
+      const int64_t col = (2 * static_cast<int64_t>(tn) + p) * (64 * HALVES);
+      uint64_t acc[32 * HALVES];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      for (int i = 0; i < 32 * HALVES; ++i) acc[i] = 0;
       for (int kb = 0; kb < KB && live; ++kb, ++it) {
         uint64_t s2 = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t buf = 2 * (it & 1) + h;
+        for (int h = 0; h < HALVES; ++h) {
+          const uint32_t buf = HALVES * (it % kDepth) + h;
           // (votes: the lanes of a warp take the same way out of an aborted launch)
           if (!__all_sync(0xFFFFFFFFu, ahead) &&
-              !__all_sync(0xFFFFFFFFu, mbar_wait(filled + 8 * buf, (it >> 1) & 1, abort_flag, args.status))) {
+              !__all_sync(0xFFFFFFFFu, mbar_wait(filled + 8 * buf, (it / kDepth) & 1, abort_flag, args.status))) {
             live = false;
             break;
           }
@@ -696,7 +737,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           tmem_ld32(taddr + 128u * buf + 32, r + 32);
           tmem_ld_wait();
           if (h == 0) {
-            const float* slot = reinterpret_cast<const float*>(base + kF8OffScale + (it % kF8ScaleRing) * kF8ScaleBytes);
+            const float* slot = reinterpret_cast<const float*>(base + C::kOffScale + (it % C::kScaleRing) * kF8ScaleBytes);
             const float s = slot[32 * q + lane] * slot[128 + p];
             asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
           }
@@ -705,7 +746,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(freed + 8 * buf);
           // whether the next product is there already, asked now and looked at after the additions
-          ahead = mbar_test(filled + 8 * (h == 0 ? buf + 1 : 2 * ((it + 1) & 1)), ((it + h) >> 1) & 1);
+          const uint32_t next = HALVES * it + h + 1;             // counted in accumulators
+          ahead = mbar_test(filled + 8 * (next % C::kAccs), (next / C::kAccs) & 1);
 #pragma unroll
           for (int i = 0; i < 32; ++i) fma_f32x2(acc[32 * h + i], r[2 * i], r[2 * i + 1], s2);
         }
@@ -716,11 +758,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       // box: by a TMA store, or by the lanes where rows are not 16-byte aligned.
       const int per = args.out_f32 ? 32 : 64;                      // columns of a box
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (!args.out_f32 && b >= 2) break;
+      for (int b = 0; b < 2 * HALVES; ++b) {
+        if (!args.out_f32 && b >= HALVES) break;
         if (lane == 0) bulk_wait_read();                           // the box before has been read
         __syncwarp();
-        QLORA_CHECK_ONLY(kF8OffStage + (warp + 1) * kF8StageBytes <= kF8OffScale, 202);
+        QLORA_CHECK_ONLY(C::kOffStage + (warp + 1) * kF8StageBytes <= C::kOffScale, 202);
         uint8_t* line = stage + lane * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -733,7 +775,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             uint32_t pk[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint64_t x = acc[(32 * b + 4 * c + i) & 63];
+              const uint64_t x = acc[(32 * b + 4 * c + i) % (32 * HALVES)];
               pk[i] = pack_bf16x2(__uint_as_float(static_cast<uint32_t>(x)), __uint_as_float(static_cast<uint32_t>(x >> 32)));
             }
             v = make_uint4(pk[0], pk[1], pk[2], pk[3]);
@@ -784,5 +826,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     tmem_dealloc_pair(tmem_d, kF8TmemCols);
   }
 }
+
+using Fp8Gemm = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Fp8GemmArgs);
 
 }  // namespace qlora

@@ -143,9 +143,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 // Named barrier that also ANDs a predicate over the participating threads.
 __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t threads, bool v) {
   uint32_t r;

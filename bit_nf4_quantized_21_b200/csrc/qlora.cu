@@ -119,16 +119,18 @@ bool ensure_smem_attrs() {
   ok = ok && cudaFuncSetAttribute(k_skinny<0, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) == cudaSuccess;
   ok = ok && cudaFuncSetAttribute(k_skinny<1, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) == cudaSuccess;
   ok = ok && cudaFuncSetAttribute(k_gemv_nf4, cudaFuncAttributeMaxDynamicSharedMemorySize, kGvSmemBytes) == cudaSuccess;
-  ok = ok && cudaFuncSetAttribute(k_fp8_gemm<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8SmemBytes) == cudaSuccess;
-  ok = ok && cudaFuncSetAttribute(k_fp8_gemm<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8SmemBytes) == cudaSuccess;
   for (const void* k : {reinterpret_cast<const void*>(k_fp8_gemv<1>), reinterpret_cast<const void*>(k_fp8_gemv<2>),
                         reinterpret_cast<const void*>(k_fp8_gemv<4>)})
     ok = ok && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) == cudaSuccess;
   // the FP8 GEMM's warps share out the registers that a launch brings: a
   // build with fewer would wait for registers that never come
-  for (const void* k : {reinterpret_cast<const void*>(k_fp8_gemm<0>), reinterpret_cast<const void*>(k_fp8_gemm<1>)}) {
+  const std::pair<Fp8Gemm, uint32_t> gemms[] = {
+      {k_fp8_gemm<0, 2>, F8Cfg<0, 2>::kSmem}, {k_fp8_gemm<1, 2>, F8Cfg<1, 2>::kSmem},
+      {k_fp8_gemm<0, 1>, F8Cfg<0, 1>::kSmem}, {k_fp8_gemm<1, 1>, F8Cfg<1, 1>::kSmem}};
+  for (const auto& g : gemms) {
     cudaFuncAttributes fa;
-    ok = ok && cudaFuncGetAttributes(&fa, k) == cudaSuccess && fa.numRegs >= kF8Regs;
+    ok = ok && cudaFuncSetAttribute(g.first, cudaFuncAttributeMaxDynamicSharedMemorySize, g.second) == cudaSuccess &&
+         cudaFuncGetAttributes(&fa, g.first) == cudaSuccess && fa.numRegs >= kF8Regs;
   }
   if (ok) done.fetch_or(bit);
   return ok;
@@ -1376,18 +1378,25 @@ qlora_status run_fp8_gemv(const qlora_fp8_matrix* Wq, const qlora_fp8_matrix* Xq
 qlora_status run_fp8_gemm(int mode, const qlora_fp8_matrix* Wq, const qlora_fp8_matrix* Aq, void* out,
                           qlora_dtype o_dtype, int64_t ldo, bool after_quant, int* status, cudaStream_t cs) {
   const int64_t M = Aq->rows, out_cols = mode == 0 ? Wq->rows : Wq->cols;
-  const int64_t tm = cdiv(M, 256), tn = cdiv(out_cols, 256);
+  const int sms = sm_count();
+  if (sms < 2) return QLORA_ERR_CUDA;
+  const int64_t tm = cdiv(M, 256);
+  // Tiles of 128 columns where all of them run at once, else of 256: a narrow
+  // tile's block takes 0.3 us against 0.48 (64 x 4096 x 4096: 16.2 against
+  // 19.0 us; 256 x 9472 x 4096, 74 narrow tiles: 18.7 against 23.0), but two
+  // rounds of them cost more than one of wide ones (256 x 11008 x 4096, 86
+  // narrow tiles: 28.1 against 23.3).
+  const int halves = tm * cdiv(out_cols, 128) <= sms / 2 ? 1 : 2;
+  const int64_t tn = cdiv(out_cols, 128 * halves);
   // tiles and a pair's blocks are counted in 32 bits
   if (tm * tn > (int64_t(1) << 28) || tm * tn * cdiv(mode == 0 ? Wq->cols : Wq->rows, kF8Block) > (int64_t(1) << 30))
     return QLORA_ERR_UNSUPPORTED;
   if (!ensure_smem_attrs()) return QLORA_ERR_CUDA;
-  const int sms = sm_count();
-  if (sms < 2) return QLORA_ERR_CUDA;
   CUtensorMap ta, tw;
   if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, Aq->codes, Aq->cols, M, Aq->ld, 128, 128,
                 CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq->codes, Wq->cols, Wq->rows, Wq->ld, 128, 128,
-                CU_TENSOR_MAP_SWIZZLE_128B))
+      !make_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq->codes, Wq->cols, Wq->rows, Wq->ld, 128,
+                mode == 0 ? 64 * halves : 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return QLORA_ERR_CUDA;
   Fp8GemmArgs a{};
   a.M = M; a.out_cols = out_cols; a.ctr = mode == 0 ? Wq->cols : Wq->rows;
@@ -1407,12 +1416,13 @@ qlora_status run_fp8_gemm(int mode, const qlora_fp8_matrix* Wq, const qlora_fp8_
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(sms / 2, tm * tn)));
   cfg.blockDim = dim3(kF8Threads);
-  cfg.dynamicSmemBytes = kF8SmemBytes;
+  cfg.dynamicSmemBytes = halves == 2 ? F8Cfg<0, 2>::kSmem : mode == 0 ? F8Cfg<0, 1>::kSmem : F8Cfg<1, 1>::kSmem;
   cfg.stream = cs;
   a.after_quant = after_quant ? 1 : 0;
   LaunchAttrs attrs(cfg, 2, after_quant);
-  const cudaError_t e = mode == 0 ? cudaLaunchKernelEx(&cfg, k_fp8_gemm<0>, ta, tw, to, a)
-                                  : cudaLaunchKernelEx(&cfg, k_fp8_gemm<1>, ta, tw, to, a);
+  const Fp8Gemm kernel = halves == 2 ? (mode == 0 ? k_fp8_gemm<0, 2> : k_fp8_gemm<1, 2>)
+                                     : (mode == 0 ? k_fp8_gemm<0, 1> : k_fp8_gemm<1, 1>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tw, to, a);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return QLORA_ERR_CUDA;

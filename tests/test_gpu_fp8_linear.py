@@ -149,6 +149,17 @@ def test_forward_and_backward_match_binary64(M, N, K, out_dtype):
     assert ((y.double() - full).norm() / full.norm()).item() <= 2.0 ** -4
 
 
+# both tile widths of the product, either side of the last count of narrow
+# tiles that all run at once, and more tiles than run at once, in each
+# direction; whole and broken scale blocks, aligned and odd rows
+@pytest.mark.parametrize("M,N,K", [
+    (256, 9472, 384), (256, 9473, 300), (300, 9500, 700), (300, 384, 9472), (256, 300, 9475), (300, 700, 9500),
+    (2600, 2600, 300), (2500, 300, 2601), (1100, 5000, 640)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_every_tile_width_and_count_matches_binary64(M, N, K, out_dtype):
+    test_forward_and_backward_match_binary64(M, N, K, out_dtype)
+
+
 def test_padding_bytes_of_the_weight_never_matter():
     N, K = 300, 200
     W = q.qlora_fp8_quantize(_normal((N, K), 0.05, 3).to(DEV))
