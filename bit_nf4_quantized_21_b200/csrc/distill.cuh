@@ -29,6 +29,11 @@
 // teacher's list, whose chain of dependent loads would otherwise be most of
 // a short row's time.  Rows may start at any element: the vector part of a row runs
 // from its first 16-byte boundary, the ragged ends element by element.
+//
+// Measured, against a copy's rate of 6.57 TB/s: loss and gradient in one call
+// 4096 x 32768 bf16 104 us (5.2 TB/s; the copy would take 82), fp32 204 us
+// (164), 1024 x 131072 bf16 120 us (82); loss alone 4096 x 32768 bf16 55 us
+// (41), 6 x 131072 5.2 us; gradient alone 777 x 50021 fp32 59 us (47).
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>

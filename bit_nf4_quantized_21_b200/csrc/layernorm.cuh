@@ -24,6 +24,14 @@
 // for every row, so its share of dw and db accumulates in registers and is
 // written once per block as a row of partials; k_ln_finish adds the partials
 // in a fixed order (no atomics: results do not depend on scheduling).
+//
+// Measured, against a copy's rate of 6.57 TB/s (bf16 unless said): forward
+// 8192 x 8192 47.3 us (5.7 TB/s; the copy would take 40.9), 4096 x 4096 12.2
+// us, 16 x 4096 3.0 us (two dependent trips to memory and a launch).
+// Backward 8192 x 8192 74 us (61.3), 4096 x 4096 24.2 us (15.3; 18.0 without
+// the parameters' gradients: writing one row of partials per block and adding
+// them up is the rest), 1237 x 2051 fp32 14.4 us (4.6; single-element loads,
+// three rows per SM).
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -296,7 +304,7 @@ __device__ __forceinline__ void ln_write_part(const LnArgs& a, int64_t group, in
 // Backward, rows in registers.  The grid walks the rows; the loads of the
 // next row are in flight while the current one is reduced.
 template <typename T, int VEC, int GROUP, int PER>
-__global__ void __launch_bounds__(ln_bwd_block<GROUP>(), GROUP <= 512 ? 2 : 1) k_ln_bwd(const LnArgs a) {
+__global__ void __launch_bounds__(ln_bwd_block<GROUP>(), PER > 8 ? 3 : GROUP <= 512 ? 2 : 1) k_ln_bwd(const LnArgs a) {
   constexpr int kRows = ln_bwd_block<GROUP>() / GROUP;
   __shared__ __align__(16) float2 red[2][32];
   const int t = threadIdx.x % GROUP;
