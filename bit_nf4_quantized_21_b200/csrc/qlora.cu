@@ -98,6 +98,21 @@ struct NvtxRange {
   NvtxRange& operator=(const NvtxRange&) = delete;
 };
 
+// Kernel attributes, set once per device.  They belong to the kernel and not
+// to a call, so `set` gives each a value that serves every call: one that
+// followed a call's size would change under another host thread between that
+// thread's setting and its launch.
+template <typename F>
+bool once_per_device(std::atomic<uint64_t>& done, F&& set) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load() & bit) return true;
+  if (!set()) return false;
+  done.fetch_or(bit);
+  return true;
+}
+
 // kernels with > 48 KB of dynamic shared memory need the opt-in once per device
 bool ensure_smem_attrs() {
   static std::atomic<uint64_t> done{0};
@@ -1528,21 +1543,26 @@ LnPlan ln_plan(int64_t cols, int vec_elems, bool vec) {
 template <typename T, int GROUP, int PER, bool BWD>
 int ln_ring(LnArgs a, int max_parts, cudaStream_t cs) {
   const int64_t slot = a.cols * static_cast<int64_t>(sizeof(T)) * (BWD ? 2 : 1);
-  const int per_sm = BWD ? (GROUP <= 256 ? 512 / GROUP : 1) : 1024 / GROUP;
-  const int64_t budget = 200 * 1024 / per_sm;
+  constexpr int per_sm = BWD ? (GROUP <= 256 ? 512 / GROUP : 1) : 1024 / GROUP;
+  constexpr int budget = 200 * 1024 / per_sm;
   a.stages = static_cast<int>(std::min<int64_t>(kLnMaxStages, budget / slot));
   const int64_t blocks = static_cast<int64_t>(sm_count()) * per_sm;
   if (a.stages < 2 || a.rows < 4 * blocks || (BWD && blocks > max_parts)) return 0;
   const bool full = a.cols == static_cast<int64_t>(GROUP) * PER * LnElem<T>::kVec;
-  void (*k)(LnArgs);
-  if constexpr (BWD) k = full ? k_ln_bwd_ring<T, GROUP, PER, true> : k_ln_bwd_ring<T, GROUP, PER, false>;
-  else k = full ? k_ln_fwd_ring<T, GROUP, PER, true> : k_ln_fwd_ring<T, GROUP, PER, false>;
-  const size_t smem = static_cast<size_t>(a.stages) * slot;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+  void (*k[2])(LnArgs);                    // rows of any length, of the full length
+  if constexpr (BWD) { k[0] = k_ln_bwd_ring<T, GROUP, PER, false>; k[1] = k_ln_bwd_ring<T, GROUP, PER, true>; }
+  else { k[0] = k_ln_fwd_ring<T, GROUP, PER, false>; k[1] = k_ln_fwd_ring<T, GROUP, PER, true>; }
+  static std::atomic<uint64_t> done{0};
+  const bool ready = once_per_device(done, [&] {
+    for (auto f : k)
+      if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, budget) != cudaSuccess) return false;
+    return true;
+  });
+  if (!ready) {
     cudaGetLastError();
     return 0;
   }
-  k<<<static_cast<unsigned>(blocks), GROUP, smem, cs>>>(a);
+  k[full]<<<static_cast<unsigned>(blocks), GROUP, static_cast<size_t>(a.stages) * slot, cs>>>(a);
   return static_cast<int>(blocks);
 }
 
