@@ -220,16 +220,23 @@ PyObject* layernorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // ------------------------------------------------------------------- FP8 layer
+// The codes of an FP8Matrix: E4M3, or plain bytes.  Every other one-byte type
+// (E5M2, the fnuz forms, int8) means something else by its bits.
+const at::Tensor& fp8_codes(PyObject* o) {
+  const at::Tensor& codes = tensor(o, "codes");
+  const auto s = codes.scalar_type();
+  TORCH_CHECK_VALUE(s == at::kByte || s == at::kFloat8_e4m3fn, "codes must be uint8 or float8_e4m3fn, got ", s);
+  return codes;
+}
 // an FP8Matrix as (rows, cols, block_rows, codes, scale)
 qlora_fp8_matrix fp8_matrix(PyObject* const* a, const Device& d) {
   qlora_fp8_matrix m{};
   m.rows = as_int(a[0]);
   m.cols = as_int(a[1]);
   m.block_rows = static_cast<int32_t>(as_int(a[2]));
-  const at::Tensor &codes = tensor(a[3], "codes"), &scale = tensor(a[4], "scale");
+  const at::Tensor &codes = fp8_codes(a[3]), &scale = tensor(a[4], "scale");
   d.same(&codes);
   d.same(&scale);
-  TORCH_CHECK_VALUE(codes.element_size() == 1, "codes are bytes");
   TORCH_CHECK_VALUE(m.rows >= 0 && m.cols >= 1 && (m.block_rows == 1 || m.block_rows == 128), "not an FP8 matrix");
   const Matrix c = matrix(codes, "codes", m.rows);
   TORCH_CHECK_VALUE(c.cols >= (m.cols + 15) / 16 * 16, "codes: a row holds cols rounded up to 16 bytes");
@@ -245,6 +252,7 @@ PyObject* fp8_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   arguments(n, 7);
   const at::Tensor& X = tensor(a[0], "X");
   Opt st = tensor_or_none(a[6], "d_status");
+  fp8_codes(a[4]);
   const Device d(X);
   d.same(st);
   const c10::cuda::CUDAGuard guard(d.dev);
@@ -264,7 +272,8 @@ PyObject* fp8_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   arguments(n, 15);
   const bool bwd = PyObject_IsTrue(a[0]) != 0;
   Opt X = tensor_or_none(a[1], "activations"), out = tensor_or_none(a[12], "output"), st = tensor_or_none(a[14], "d_status");
-  const Device d(tensor(a[10], "codes"));
+  if (a[2] != Py_None) fp8_codes(a[5]);
+  const Device d(fp8_codes(a[10]));
   for (Opt t : {X, out, st}) d.same(t);
   const c10::cuda::CUDAGuard guard(d.dev);
   const qlora_fp8_matrix W = fp8_matrix(a + 7, d);

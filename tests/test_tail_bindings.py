@@ -1,0 +1,34 @@
+"""Host-side checks, without a GPU, of the compiled binding and of what the
+library settles before it enqueues anything."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import bit_nf4_quantized_21_b200 as q
+
+
+def _matrix(dtype, rows=128, cols=64, block_rows=128):
+    m = q.empty_fp8(rows, cols, "cpu", block_rows)
+    m.codes = m.codes.view(dtype)
+    return m
+
+
+# Only the type is looked at before the device: codes of the right type are
+# then refused as host tensors.
+@pytest.mark.parametrize("dtype,wrong", [
+    (torch.float8_e5m2, True), (torch.float8_e4m3fnuz, True), (torch.float8_e5m2fnuz, True), (torch.int8, True),
+    (torch.bool, True), (torch.uint8, False), (torch.float8_e4m3fn, False)])
+def test_fp8_codes_are_e4m3_or_bytes(dtype, wrong):
+    message = "codes must be uint8 or float8_e4m3fn" if wrong else "CUDA tensors only"
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError, match=message):
+        q.qlora_fp8_quantize(x, out=_matrix(dtype, 4, 64, 1))
+    with pytest.raises(ValueError, match=message):
+        q.qlora_fp8_linear_fwd(x, _matrix(dtype))
+    with pytest.raises(ValueError, match=message):
+        q.qlora_fp8_linear_bwd(torch.zeros(4, 128), _matrix(dtype))
+    with pytest.raises(ValueError, match=message):           # the activations' codes, as scratch and as input
+        q.qlora_fp8_linear_fwd(x, _matrix(torch.uint8), Xq=_matrix(dtype, 4, 64, 1))
+    with pytest.raises(ValueError, match=message):
+        q.qlora_fp8_linear_fwd(_matrix(dtype, 4, 64, 1), _matrix(torch.uint8))
