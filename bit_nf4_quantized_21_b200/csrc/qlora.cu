@@ -1373,7 +1373,6 @@ qlora_status run_fp8_gemv(const qlora_fp8_matrix* Wq, const qlora_fp8_matrix* Xq
   a.x = Xq->codes; a.ldx = Xq->ld; a.M = static_cast<int>(Xq->rows); a.sx = Xq->scale;
   a.y = Y; a.ldy = ldy; a.y_f32 = y_dtype == QLORA_F32 ? 1 : 0;
   a.after_quant = after_quant ? 1 : 0;
-  if (!ensure_smem_attrs()) return QLORA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(std::max(1, sm_count()), cdiv(a.N, kF8GemvRows))));
   cfg.blockDim = dim3(kF8GemvThreads);
@@ -1390,11 +1389,19 @@ qlora_status run_fp8_gemv(const qlora_fp8_matrix* Wq, const qlora_fp8_matrix* Xq
   return QLORA_OK;
 }
 
-qlora_status run_fp8_gemm(int mode, const qlora_fp8_matrix* Wq, const qlora_fp8_matrix* Aq, void* out,
-                          qlora_dtype o_dtype, int64_t ldo, bool after_quant, int* status, cudaStream_t cs) {
+// A launch of the many-token product.  Everything that can refuse the call is
+// settled here, before the quantiser goes to the stream ahead of it.
+struct Fp8GemmPlan {
+  CUtensorMap act, w, out;
+  Fp8GemmArgs args;
+  Fp8Gemm kernel;
+  unsigned grid;
+  size_t smem;
+};
+qlora_status plan_fp8_gemm(int mode, const qlora_fp8_matrix* Wq, const qlora_fp8_matrix* Aq, void* out,
+                           qlora_dtype o_dtype, int64_t ldo, int* status, Fp8GemmPlan& p) {
   const int64_t M = Aq->rows, out_cols = mode == 0 ? Wq->rows : Wq->cols;
   const int sms = sm_count();
-  if (sms < 2) return QLORA_ERR_CUDA;
   const int64_t tm = cdiv(M, 256);
   // Tiles of 128 columns where all of them run at once, else of 256: a narrow
   // tile's block takes 0.3 us against 0.48 (64 x 4096 x 4096: 16.2 against
@@ -1406,38 +1413,44 @@ qlora_status run_fp8_gemm(int mode, const qlora_fp8_matrix* Wq, const qlora_fp8_
   // tiles and a pair's blocks are counted in 32 bits
   if (tm * tn > (int64_t(1) << 28) || tm * tn * cdiv(mode == 0 ? Wq->cols : Wq->rows, kF8Block) > (int64_t(1) << 30))
     return QLORA_ERR_UNSUPPORTED;
-  if (!ensure_smem_attrs()) return QLORA_ERR_CUDA;
-  CUtensorMap ta, tw;
-  if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, Aq->codes, Aq->cols, M, Aq->ld, 128, 128,
+  if (sms < 2 || !ensure_smem_attrs()) return QLORA_ERR_CUDA;
+  if (!make_map(&p.act, CU_TENSOR_MAP_DATA_TYPE_UINT8, Aq->codes, Aq->cols, M, Aq->ld, 128, 128,
                 CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq->codes, Wq->cols, Wq->rows, Wq->ld, 128,
+      !make_map(&p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq->codes, Wq->cols, Wq->rows, Wq->ld, 128,
                 mode == 0 ? 64 * halves : 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return QLORA_ERR_CUDA;
-  Fp8GemmArgs a{};
+  Fp8GemmArgs& a = p.args;
+  a = Fp8GemmArgs{};
   a.M = M; a.out_cols = out_cols; a.ctr = mode == 0 ? Wq->cols : Wq->rows;
   a.sa = Aq->scale; a.sw = Wq->scale; a.sw_cols = cdiv(Wq->cols, kF8Block);
   a.out = out; a.ldo = ldo; a.out_f32 = o_dtype == QLORA_F32 ? 1 : 0;
   // whole boxes go out by TMA where every output row is 16-byte aligned
-  CUtensorMap to = ta;
+  p.out = p.act;
   if (rows16(out, ldo, dtype_size(o_dtype))) {
     const bool f32 = o_dtype == QLORA_F32;
-    if (!make_map(&to, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, out_cols, M,
+    if (!make_map(&p.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, out_cols, M,
                   static_cast<uint64_t>(ldo) * dtype_size(o_dtype), f32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
       return QLORA_ERR_CUDA;
     a.tma_out = 1;
   }
   a.tiles_m = static_cast<int>(tm); a.tiles_n = static_cast<int>(tn);
   a.status = status;
+  p.grid = static_cast<unsigned>(2 * std::min<int64_t>(sms / 2, tm * tn));
+  p.smem = halves == 2 ? F8Cfg<0, 2>::kSmem : mode == 0 ? F8Cfg<0, 1>::kSmem : F8Cfg<1, 1>::kSmem;
+  p.kernel = halves == 2 ? (mode == 0 ? k_fp8_gemm<0, 2> : k_fp8_gemm<1, 2>)
+                         : (mode == 0 ? k_fp8_gemm<0, 1> : k_fp8_gemm<1, 1>);
+  return QLORA_OK;
+}
+
+qlora_status run_fp8_gemm(Fp8GemmPlan& p, bool after_quant, cudaStream_t cs) {
+  p.args.after_quant = after_quant ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(sms / 2, tm * tn)));
+  cfg.gridDim = dim3(p.grid);
   cfg.blockDim = dim3(kF8Threads);
-  cfg.dynamicSmemBytes = halves == 2 ? F8Cfg<0, 2>::kSmem : mode == 0 ? F8Cfg<0, 1>::kSmem : F8Cfg<1, 1>::kSmem;
+  cfg.dynamicSmemBytes = p.smem;
   cfg.stream = cs;
-  a.after_quant = after_quant ? 1 : 0;
   LaunchAttrs attrs(cfg, 2, after_quant);
-  const Fp8Gemm kernel = halves == 2 ? (mode == 0 ? k_fp8_gemm<0, 2> : k_fp8_gemm<1, 2>)
-                                     : (mode == 0 ? k_fp8_gemm<0, 1> : k_fp8_gemm<1, 1>);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tw, to, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, p.kernel, p.act, p.w, p.out, p.args);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return QLORA_ERR_CUDA;
@@ -1459,12 +1472,17 @@ qlora_status fp8_linear(int mode, const void* X, qlora_dtype x_dtype, int64_t ld
   if (X && (!is_io_dtype(x_dtype) || ldx < in_cols || !aligned_to(X, dtype_size(x_dtype)))) return QLORA_ERR_INVALID_ARG;
   if (Xq->rows == 0) return QLORA_OK;
   if (!Y || !aligned_to(Y, dtype_size(y_dtype))) return QLORA_ERR_INVALID_ARG;
+  const bool gemv = mode == 0 && fp8_takes_gemv(Xq->rows, Xq->cols);
+  Fp8GemmPlan plan;
+  st = !gemv                 ? plan_fp8_gemm(mode, Wq, Xq, Y, y_dtype, ldy, status, plan)
+       : ensure_smem_attrs() ? QLORA_OK
+                             : QLORA_ERR_CUDA;
+  if (st != QLORA_OK) return st;
   if (X) {
     st = run_fp8_quantize(X, x_dtype, ldx, Xq, status, cs);
     if (st != QLORA_OK) return st;
   }
-  if (mode == 0 && fp8_takes_gemv(Xq->rows, Xq->cols)) return run_fp8_gemv(Wq, Xq, Y, y_dtype, ldy, X != nullptr, cs);
-  return run_fp8_gemm(mode, Wq, Xq, Y, y_dtype, ldy, X != nullptr, status, cs);
+  return gemv ? run_fp8_gemv(Wq, Xq, Y, y_dtype, ldy, X != nullptr, cs) : run_fp8_gemm(plan, X != nullptr, cs);
 }
 
 }  // namespace

@@ -2,10 +2,13 @@
 library settles before it enqueues anything."""
 from __future__ import annotations
 
+import ctypes
+
 import pytest
 import torch
 
 import bit_nf4_quantized_21_b200 as q
+from bit_nf4_quantized_21_b200 import qlora as binding
 
 
 def _matrix(dtype, rows=128, cols=64, block_rows=128):
@@ -32,3 +35,28 @@ def test_fp8_codes_are_e4m3_or_bytes(dtype, wrong):
         q.qlora_fp8_linear_fwd(x, _matrix(torch.uint8), Xq=_matrix(dtype, 4, 64, 1))
     with pytest.raises(ValueError, match=message):
         q.qlora_fp8_linear_fwd(_matrix(dtype, 4, 64, 1), _matrix(torch.uint8))
+
+
+# ------------------------------------------- nothing is enqueued by a call that is refused
+
+FAKE = 1 << 40                      # an aligned device address that nothing reads
+UNSUPPORTED = 2
+
+
+def _c(rows, cols, block_rows):
+    return binding.FP8MatrixC(rows, cols, -(-cols // 128) * 128, block_rows, 0, FAKE, FAKE)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="shown by a status that only a machine without a device gives")
+@pytest.mark.parametrize("quantise", [True, False])
+def test_fp8_products_with_too_many_tiles_are_refused_first(quantise):
+    """2^22 rows of tiles by 2^8 columns of them: more than the product counts.  The
+    quantiser alone would take these activations, so the refusal has to come before it;
+    here its launch would fail, for want of a device, with another status."""
+    L = q.lib()
+    M, N, K = 1 << 30, 1 << 16, 128
+    X = FAKE if quantise else None
+    W, A = _c(N, K, 128), _c(M, K, 1)
+    assert L.qlora_fp8_linear_fwd(X, 1, K, ctypes.byref(W), ctypes.byref(A), FAKE, 1, N, None, None) == UNSUPPORTED
+    W, A = _c(K, N, 128), _c(M, K, 1)
+    assert L.qlora_fp8_linear_bwd(X, 1, K, ctypes.byref(W), ctypes.byref(A), FAKE, 1, N, None, None) == UNSUPPORTED
