@@ -108,47 +108,39 @@ bool once_per_device(std::atomic<uint64_t>& done, F&& set) {
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const uint64_t bit = 1ull << (dev & 63);
   if (done.load() & bit) return true;
-  if (!set()) return false;
+  if (!set()) {
+    cudaGetLastError();   // (the next call does not report this one's error)
+    return false;
+  }
   done.fetch_or(bit);
   return true;
 }
 
-// kernels with > 48 KB of dynamic shared memory need the opt-in once per device
+bool set_smem(const void* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+template <typename... A>
+bool set_smem(void (*kernel)(A...), int bytes) {
+  return set_smem(reinterpret_cast<const void*>(kernel), bytes);
+}
+constexpr int kMaxSmem = 227 * 1024;
+
+// kernels with > 48 KB of dynamic shared memory need the opt-in
 bool ensure_smem_attrs() {
   static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (done.load() & bit) return true;
-  const int max_smem = 227 * 1024;
-  bool ok = cudaFuncSetAttribute(k_gemm_nf4<kModeFwd>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemBytes) == cudaSuccess;
-  ok = ok && cudaFuncSetAttribute(k_gemm_nf4<kModeDx>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemBytes) == cudaSuccess;
-  const void* pair_kernels[] = {
-      reinterpret_cast<const void*>(k_gemm_nf4_pair<kModeFwd, false, 1>), reinterpret_cast<const void*>(k_gemm_nf4_pair<kModeDx, false, 1>),
-      reinterpret_cast<const void*>(k_gemm_nf4_pair<kModeFwd, true, 1>), reinterpret_cast<const void*>(k_gemm_nf4_pair<kModeDx, true, 1>),
-      reinterpret_cast<const void*>(k_gemm_nf4_pair<kModeFwd, false, 2>), reinterpret_cast<const void*>(k_gemm_nf4_pair<kModeDx, false, 2>),
-      reinterpret_cast<const void*>(k_gemm_nf4_pair<kModeFwd, true, 2>), reinterpret_cast<const void*>(k_gemm_nf4_pair<kModeDx, true, 2>)};
-  for (const void* k : pair_kernels)
-    ok = ok && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmemBytes) == cudaSuccess;
-  ok = ok && cudaFuncSetAttribute(k_skinny<0, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) == cudaSuccess;
-  ok = ok && cudaFuncSetAttribute(k_skinny<0, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) == cudaSuccess;
-  ok = ok && cudaFuncSetAttribute(k_skinny<1, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) == cudaSuccess;
-  ok = ok && cudaFuncSetAttribute(k_gemv_nf4, cudaFuncAttributeMaxDynamicSharedMemorySize, kGvSmemBytes) == cudaSuccess;
-  for (const void* k : {reinterpret_cast<const void*>(k_fp8_gemv<1>), reinterpret_cast<const void*>(k_fp8_gemv<2>),
-                        reinterpret_cast<const void*>(k_fp8_gemv<4>)})
-    ok = ok && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) == cudaSuccess;
-  // the FP8 GEMM's warps share out the registers that a launch brings: a
-  // build with fewer would wait for registers that never come
-  const std::pair<Fp8Gemm, uint32_t> gemms[] = {
-      {k_fp8_gemm<0, 2>, F8Cfg<0, 2>::kSmem}, {k_fp8_gemm<1, 2>, F8Cfg<1, 2>::kSmem},
-      {k_fp8_gemm<0, 1>, F8Cfg<0, 1>::kSmem}, {k_fp8_gemm<1, 1>, F8Cfg<1, 1>::kSmem}};
-  for (const auto& g : gemms) {
-    cudaFuncAttributes fa;
-    ok = ok && cudaFuncSetAttribute(g.first, cudaFuncAttributeMaxDynamicSharedMemorySize, g.second) == cudaSuccess &&
-         cudaFuncGetAttributes(&fa, g.first) == cudaSuccess && fa.numRegs >= kF8Regs;
-  }
-  if (ok) done.fetch_or(bit);
-  return ok;
+  return once_per_device(done, [] {
+    return set_smem(k_gemm_nf4<kModeFwd>, kGemmSmemBytes) && set_smem(k_gemm_nf4<kModeDx>, kGemmSmemBytes) &&
+           set_smem(k_gemm_nf4_pair<kModeFwd, false, 1>, kPairSmemBytes) &&
+           set_smem(k_gemm_nf4_pair<kModeDx, false, 1>, kPairSmemBytes) &&
+           set_smem(k_gemm_nf4_pair<kModeFwd, true, 1>, kPairSmemBytes) &&
+           set_smem(k_gemm_nf4_pair<kModeDx, true, 1>, kPairSmemBytes) &&
+           set_smem(k_gemm_nf4_pair<kModeFwd, false, 2>, kPairSmemBytes) &&
+           set_smem(k_gemm_nf4_pair<kModeDx, false, 2>, kPairSmemBytes) &&
+           set_smem(k_gemm_nf4_pair<kModeFwd, true, 2>, kPairSmemBytes) &&
+           set_smem(k_gemm_nf4_pair<kModeDx, true, 2>, kPairSmemBytes) && set_smem(k_skinny<0, 0>, kMaxSmem) &&
+           set_smem(k_skinny<0, 1>, kMaxSmem) && set_smem(k_skinny<1, 1>, kMaxSmem) &&
+           set_smem(k_gemv_nf4, kGvSmemBytes);
+  });
 }
 
 // streaming multiprocessors of the current device (cached per device)
@@ -1340,14 +1332,35 @@ qlora_status run_fp8_quantize(const void* X, qlora_dtype dt, int64_t ldx, const 
   return check_launch();
 }
 
+// The same for the FP8 kernels, by themselves: what they refuse to be launched
+// with is no reason for another layer's call to fail.  The GEMM's warps share
+// out the registers that a launch brings: a build with fewer would wait for
+// registers that never come.
+bool ensure_fp8_attrs() {
+  static std::atomic<uint64_t> done{0};
+  return once_per_device(done, [] {
+    if (!set_smem(k_fp8_gemv<1>, kMaxSmem) || !set_smem(k_fp8_gemv<2>, kMaxSmem) || !set_smem(k_fp8_gemv<4>, kMaxSmem))
+      return false;
+    const std::pair<Fp8Gemm, uint32_t> gemms[] = {
+        {k_fp8_gemm<0, 2>, F8Cfg<0, 2>::kSmem}, {k_fp8_gemm<1, 2>, F8Cfg<1, 2>::kSmem},
+        {k_fp8_gemm<0, 1>, F8Cfg<0, 1>::kSmem}, {k_fp8_gemm<1, 1>, F8Cfg<1, 1>::kSmem}};
+    for (const auto& g : gemms) {
+      cudaFuncAttributes fa;
+      if (!set_smem(g.first, static_cast<int>(g.second)) || cudaFuncGetAttributes(&fa, g.first) != cudaSuccess ||
+          fa.numRegs < kF8Regs)
+        return false;
+    }
+    return true;
+  });
+}
+
 // Up to this many tokens, and as long as their codes fit in shared memory,
 // the forward takes the weight-streaming kernel.
 constexpr int64_t kF8GemvMaxM = 32;
-constexpr uint32_t kF8GemvMaxSmem = 227 * 1024;
 int fp8_gemv_nt(int64_t M) { return M <= 8 ? 1 : M <= 16 ? 2 : 4; }
 bool fp8_takes_gemv(int64_t M, int64_t K) {
   return M <= kF8GemvMaxM && K < (int64_t(1) << 20) &&
-         fp8_gemv_smem(static_cast<int>(M), K, fp8_gemv_nt(M)).bytes <= kF8GemvMaxSmem;
+         fp8_gemv_smem(static_cast<int>(M), K, fp8_gemv_nt(M)).bytes <= static_cast<uint32_t>(kMaxSmem);
 }
 
 // Launch attributes: a cluster of `cluster` CTAs, and, behind the quantiser,
@@ -1413,7 +1426,7 @@ qlora_status plan_fp8_gemm(int mode, const qlora_fp8_matrix* Wq, const qlora_fp8
   // tiles and a pair's blocks are counted in 32 bits
   if (tm * tn > (int64_t(1) << 28) || tm * tn * cdiv(mode == 0 ? Wq->cols : Wq->rows, kF8Block) > (int64_t(1) << 30))
     return QLORA_ERR_UNSUPPORTED;
-  if (sms < 2 || !ensure_smem_attrs()) return QLORA_ERR_CUDA;
+  if (sms < 2 || !ensure_fp8_attrs()) return QLORA_ERR_CUDA;
   if (!make_map(&p.act, CU_TENSOR_MAP_DATA_TYPE_UINT8, Aq->codes, Aq->cols, M, Aq->ld, 128, 128,
                 CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq->codes, Wq->cols, Wq->rows, Wq->ld, 128,
@@ -1474,9 +1487,9 @@ qlora_status fp8_linear(int mode, const void* X, qlora_dtype x_dtype, int64_t ld
   if (!Y || !aligned_to(Y, dtype_size(y_dtype))) return QLORA_ERR_INVALID_ARG;
   const bool gemv = mode == 0 && fp8_takes_gemv(Xq->rows, Xq->cols);
   Fp8GemmPlan plan;
-  st = !gemv                 ? plan_fp8_gemm(mode, Wq, Xq, Y, y_dtype, ldy, status, plan)
-       : ensure_smem_attrs() ? QLORA_OK
-                             : QLORA_ERR_CUDA;
+  st = !gemv                ? plan_fp8_gemm(mode, Wq, Xq, Y, y_dtype, ldy, status, plan)
+       : ensure_fp8_attrs() ? QLORA_OK
+                            : QLORA_ERR_CUDA;
   if (st != QLORA_OK) return st;
   if (X) {
     st = run_fp8_quantize(X, x_dtype, ldx, Xq, status, cs);
@@ -1572,14 +1585,9 @@ int ln_ring(LnArgs a, int max_parts, cudaStream_t cs) {
   else { k[0] = k_ln_fwd_ring<T, GROUP, PER, false>; k[1] = k_ln_fwd_ring<T, GROUP, PER, true>; }
   static std::atomic<uint64_t> done{0};
   const bool ready = once_per_device(done, [&] {
-    for (auto f : k)
-      if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, budget) != cudaSuccess) return false;
-    return true;
+    return set_smem(k[0], budget) && set_smem(k[1], budget);
   });
-  if (!ready) {
-    cudaGetLastError();
-    return 0;
-  }
+  if (!ready) return 0;
   k[full]<<<static_cast<unsigned>(blocks), GROUP, static_cast<size_t>(a.stages) * slot, cs>>>(a);
   return static_cast<int>(blocks);
 }

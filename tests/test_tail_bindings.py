@@ -3,6 +3,7 @@ library settles before it enqueues anything."""
 from __future__ import annotations
 
 import ctypes
+import os
 
 import pytest
 import torch
@@ -60,3 +61,22 @@ def test_fp8_products_with_too_many_tiles_are_refused_first(quantise):
     assert L.qlora_fp8_linear_fwd(X, 1, K, ctypes.byref(W), ctypes.byref(A), FAKE, 1, N, None, None) == UNSUPPORTED
     W, A = _c(K, N, 128), _c(M, K, 1)
     assert L.qlora_fp8_linear_bwd(X, 1, K, ctypes.byref(W), ctypes.byref(A), FAKE, 1, N, None, None) == UNSUPPORTED
+
+
+def _body(source, head):
+    """The text of a function, from its head to the brace that closes it."""
+    at = source.index(head)
+    return source[at:source.index("\n}\n", at)]
+
+
+def test_the_nf4_layer_does_not_hang_on_the_fp8_kernels():
+    """What readies the NF4 kernels looks at none of the FP8 ones: a build of those that the
+    library will not launch (too few registers to share out) refuses FP8 calls, nothing else."""
+    with open(os.path.join(os.path.dirname(binding.__file__), "csrc", "qlora.cu")) as f:
+        source = f.read()
+    old, new = _body(source, "bool ensure_smem_attrs() {"), _body(source, "bool ensure_fp8_attrs() {")
+    assert "k_gemm_nf4" in old and "k_skinny" in old and "fp8" not in old.lower() and "f8" not in old.lower()
+    assert "k_fp8_gemm" in new and "k_fp8_gemv" in new and "numRegs" in new
+    for head in ("qlora_status plan_fp8_gemm(", "qlora_status fp8_linear("):
+        body = _body(source, head)
+        assert "ensure_fp8_attrs()" in body and "ensure_smem_attrs()" not in body
