@@ -1,6 +1,6 @@
 """Build libqlora.so in-tree for sm_100a with nvcc, its debug build
 libqlora_debug.so (-DQLORA_DEBUG_CHECKS: index-range checks in the kernels),
-and with g++ the compiled part of the Python binding, _calls.so.
+and with g++ the compiled part of the Python binding, module _calls.
 
     python -m bit_nf4_quantized_21_b200.build        # rebuild when sources changed
     python -m bit_nf4_quantized_21_b200.build -v     # also print ptxas resource usage
@@ -19,7 +19,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqlora.so")
 LIB_DEBUG = os.path.join(PKG, "libqlora_debug.so")
-CALLS = os.path.join(PKG, "_calls.so")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -57,24 +56,40 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     return lib
 
 
+def calls_path() -> str:
+    """Where the binding of this interpreter and this torch lies.  Its code depends on the layouts of
+    both, so both are in its name: another one's binary is not there to be loaded."""
+    import torch
+    return os.path.join(PKG, f"_calls.torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def _calls_sources():
+    return [os.path.join(CSRC, "calls.cpp"), os.path.join(INCLUDE, "qlora.h")]
+
+
+def calls_need_build() -> bool:
+    path = calls_path()
+    return not os.path.exists(path) or any(os.path.getmtime(s) > os.path.getmtime(path) for s in _calls_sources())
+
+
 def build_calls(force: bool = False) -> str:
-    """_calls.so: host code against the headers and libraries of the installed torch."""
-    sources = [os.path.join(CSRC, "calls.cpp"), os.path.join(INCLUDE, "qlora.h")]
-    if not force and os.path.exists(CALLS) and all(os.path.getmtime(s) <= os.path.getmtime(CALLS) for s in sources):
-        return CALLS
+    """Module _calls: host code against the headers and libraries of the installed torch."""
+    path = calls_path()
+    if not force and not calls_need_build():
+        return path
     import torch
     torch_dir = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME") or "/usr/local/cuda"
     include = [INCLUDE, os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include/torch/csrc/api/include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-    tmp = CALLS + f".{os.getpid()}.tmp"
+    tmp = path + f".{os.getpid()}.tmp"
     # the compiler that nvcc uses too: one that links libstdc++ statically would put a second copy beside torch's
     subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wno-attributes",
-                    *(f for d in include for f in ("-isystem", d)), "-o", tmp, sources[0],
+                    *(f for d in include for f in ("-isystem", d)), "-o", tmp, _calls_sources()[0],
                     "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ldl"],
                    check=True)
-    os.replace(tmp, CALLS)
-    return CALLS
+    os.replace(tmp, path)
+    return path
 
 
 if __name__ == "__main__":

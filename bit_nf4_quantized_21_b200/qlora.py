@@ -4,12 +4,14 @@ FP8 layer, the layer norm and the distillation loss the compiled _calls).
 Every function here has the name of the C entry point it calls
 (include/qlora.h) and does nothing but turn torch tensors into device
 pointers, pick up the current CUDA stream, call the library and raise on a
-non-OK status.  There is no fallback path: if libqlora.so (or _calls.so) is missing, or a
+non-OK status.  There is no fallback path: if libqlora.so (or _calls) is missing, or a
 tensor is not on a CUDA device, the call raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from dataclasses import dataclass
@@ -536,14 +538,19 @@ def _calls():
     """The compiled marshalling, on the same libqlora build as lib()."""
     global _calls_mod
     if _calls_mod is None:
+        from .build import calls_path
         lib()
-        try:
-            from . import _calls as m
-        except ImportError as e:
-            raise RuntimeError("the compiled binding _calls.so is missing; build it with "
-                               "`python -m bit_nf4_quantized_21_b200.build`") from e
-        m.init(LIB_PATH)
-        _calls_mod = m
+        path = calls_path()
+        with _lock:
+            if _calls_mod is None:
+                if not os.path.exists(path):
+                    raise RuntimeError(f"the compiled binding of this Python and torch is missing ({path}); build it "
+                                       "with `python -m bit_nf4_quantized_21_b200.build`")
+                loader = importlib.machinery.ExtensionFileLoader(__package__ + "._calls", path)
+                m = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+                loader.exec_module(m)
+                m.init(LIB_PATH)
+                _calls_mod = m
     return _calls_mod
 
 

@@ -4,12 +4,13 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sysconfig
 
 import pytest
 import torch
 
 import bit_nf4_quantized_21_b200 as q
-from bit_nf4_quantized_21_b200 import qlora as binding
+from bit_nf4_quantized_21_b200 import build, qlora as binding
 
 
 def _matrix(dtype, rows=128, cols=64, block_rows=128):
@@ -80,3 +81,20 @@ def test_the_nf4_layer_does_not_hang_on_the_fp8_kernels():
     for head in ("qlora_status plan_fp8_gemm(", "qlora_status fp8_linear("):
         body = _body(source, head)
         assert "ensure_fp8_attrs()" in body and "ensure_smem_attrs()" not in body
+
+
+# ---------------------------------------------- the binary of the interpreter and torch at hand
+
+def test_another_torch_or_python_does_not_take_a_binding_built_for_this_one(monkeypatch):
+    path = build.build_calls()
+    assert os.path.exists(path) and not build.calls_need_build()
+    monkeypatch.setattr(binding, "_calls_mod", None)
+    assert binding._calls().layernorm_fwd is not None
+    for module, name, value in ((torch, "__version__", "2.99.0+cu999"),
+                                (sysconfig, "get_config_var", lambda _: ".cpython-399-x86_64-linux-gnu.so")):
+        with monkeypatch.context() as m:
+            m.setattr(module, name, value)
+            m.setattr(binding, "_calls_mod", None)
+            assert build.calls_path() != path and build.calls_need_build()
+            with pytest.raises(RuntimeError, match="build it with"):
+                binding._calls()
