@@ -13,9 +13,10 @@
 //
 // One sweep computes the running maximum m and the sum of exp((z - m) / tau)
 // together, fp32 throughout: exponentials in base 2 of (z - m) log2(e) / tau.
-// The maximum is subtracted before the scale is applied, so logits masked
-// with the type's lowest value neither overflow nor, where a row holds
-// nothing else, make anything but a uniform softmax.  The gradient is a second sweep over
+// The maximum is subtracted before the scale is applied, the student's and the
+// teacher's alike, so logits masked with the type's lowest value neither
+// overflow nor, where a row or a list holds nothing else, make anything but a
+// uniform softmax.  The gradient is a second sweep over
 // the row, which by then sits in L2 (rows in flight: a few per SM, tens of
 // MB in 126 MB), so a call that returns both reads the logits from memory
 // once.  Bound: HBM (one read, and one write of the gradient), closely
@@ -164,7 +165,7 @@ template <typename T, bool FWD>
 __global__ void __launch_bounds__(kDiThreads, 4) k_distill(const DistillArgs a) {
   constexpr int N = DiVec<T>::N;
   __shared__ __align__(16) int s_id[kDiMaxTop];     // vocabulary index, or -1
-  __shared__ float s_t[kDiMaxTop];                  // t / tau
+  __shared__ float s_t[kDiMaxTop];                  // t, then (t - the largest) / tau
   __shared__ float s_p[kDiMaxTop];                  // p
   __shared__ float s_z[kDiMaxTop];                  // the student's logit at the entry
   __shared__ float2 red[kDiWarps];                  // the warps' (max, sum)
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kDiThreads, 4) k_distill(const DistillArgs a) 
   const f32x2 scale = pair2(a.scale2, a.scale2);
 
   DiSum acc{-INFINITY, 0.0f};
-  float tref = 0.0f, tsum = 0.0f;
+  float tsum = 0.0f;
   if (teacher) {
     // -------------------------------------------------------- the teacher
     float tmax = -INFINITY;
@@ -202,8 +203,8 @@ __global__ void __launch_bounds__(kDiThreads, 4) k_distill(const DistillArgs a) 
     for (int j = lane; j < a.top; j += 32) {
       const int64_t e = row * a.top + j;
       const int64_t id = a.ids64 ? static_cast<const int64_t*>(a.ids)[e] : static_cast<const int32_t*>(a.ids)[e];
-      const float t = (a.t_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.t)[e])
-                                : static_cast<const float*>(a.t)[e]) / a.tau;
+      const float t = a.t_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.t)[e])
+                               : static_cast<const float*>(a.t)[e];
       const bool ok = id >= 0 && id < a.vocab;
       bad |= id >= a.vocab;
       s_id[j] = ok ? static_cast<int>(id) : -1;
@@ -214,9 +215,11 @@ __global__ void __launch_bounds__(kDiThreads, 4) k_distill(const DistillArgs a) 
     if (lane < 4 && a.top + lane < kDiMaxTop) s_id[a.top + lane] = -1;   // the scan below reads whole groups of four
     if (bad && a.status) atomicOr(a.status, QLORA_DEV_INDEX);
     tmax = di_warp_max(tmax);
-    tref = tmax == -INFINITY ? 0.0f : tmax;
+    const float tref = tmax == -INFINITY ? 0.0f : tmax;
     for (int j = lane; j < a.top; j += 32) {
-      const float e = s_id[j] >= 0 ? expf(s_t[j] - tref) : 0.0f;
+      const float d = (s_t[j] - tref) / a.tau;       // (t / tau first would overflow for the type's lowest and highest values)
+      const float e = s_id[j] >= 0 ? expf(d) : 0.0f;
+      s_t[j] = d;
       s_p[j] = e;
       tsum += e;
     }
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(kDiThreads, 4) k_distill(const DistillArgs a) 
       for (int j = lane; j < a.top; j += 32) {
         const float p = s_p[j];
         // p = 0 contributes nothing even where q = 0; a NaN p stays
-        if (!(p == 0.0f)) kl += p * (((s_t[j] - tref) - tlog) - ((s_z[j] - ref) / a.tau - zlog));
+        if (!(p == 0.0f)) kl += p * ((s_t[j] - tlog) - ((s_z[j] - ref) / a.tau - zlog));
       }
       kl = di_warp_sum(kl);
       if (lane == 0) {
