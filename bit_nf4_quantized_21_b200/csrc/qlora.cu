@@ -1769,8 +1769,8 @@ qlora_status check_distill(const void* Z, int64_t ldz, int64_t rows, int64_t voc
                            const void* dZ, int64_t lddz) {
   if (rows < 0 || vocab < 1 || ldz < vocab || !is_io_dtype(dtype) || !is_io_dtype(t_dtype)) return QLORA_ERR_INVALID_ARG;
   if ((id_bits != 32 && id_bits != 64) || top < 1 || top > kDiMaxTop) return QLORA_ERR_INVALID_ARG;
-  if (!std::isfinite(tau) || !(tau > 0.0f) || !std::isfinite(1.0f / tau) || !std::isfinite(tau * tau))
-    return QLORA_ERR_INVALID_ARG;
+  // tau^2 is a factor of the loss: it must keep its bits (which also keeps log2(e) / tau finite)
+  if (!(tau > 0.0f) || !std::isnormal(tau * tau)) return QLORA_ERR_INVALID_ARG;
   if (dZ && lddz < vocab) return QLORA_ERR_INVALID_ARG;
   if (vocab >= (int64_t(1) << 31) || rows > (int64_t(1) << 27)) return QLORA_ERR_UNSUPPORTED;
   if (rows == 0) return QLORA_OK;

@@ -448,7 +448,8 @@ qlora_status qlora_layernorm_bwd(const void* dY, int64_t lddy, const void* X, in
  * Z, dZ: `dtype` (fp32 or bf16), ldz / lddz elements between rows, aligned
  * to their element; ids [rows, top]: int32 (id_bits = 32) or int64 (64); t
  * [rows, top]: t_dtype fp32 or bf16; w (row_weight) and g (grad_loss): fp32
- * [rows], NULL = ones; tau > 0, finite; 1 <= top <= 1024; vocab < 2^31.
+ * [rows], NULL = ones; tau > 0 with tau^2 a normal fp32 number (1.1e-19 to
+ * 1.8e19; refused otherwise); 1 <= top <= 1024; vocab < 2^31.
  * A negative id marks an unused place; an id >= vocab is left out too and
  * sets QLORA_DEV_INDEX_BIT.  A teacher logit of -inf has p = 0 and
  * contributes nothing; an entry with p > 0 at a student logit of -inf makes

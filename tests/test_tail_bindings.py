@@ -98,3 +98,17 @@ def test_another_torch_or_python_does_not_take_a_binding_built_for_this_one(monk
             assert build.calls_path() != path and build.calls_need_build()
             with pytest.raises(RuntimeError, match="build it with"):
                 binding._calls()
+
+
+# ------------------------------------------------------------------ temperatures
+
+@pytest.mark.parametrize("tau,refused", [
+    (1e-17, False), (1.1e-19, False), (1.0, False), (1.8e19, False),
+    (1e-19, True), (1e-20, True), (1e-23, True), (4e-39, True), (1.9e19, True)])
+def test_temperatures_whose_square_is_no_normal_number_are_refused(tau, refused):
+    """The loss carries tau^2: where that is subnormal or 0 in fp32, the loss of a row
+    (of the size of tau |z|) would come out short of bits, or as 0.  No rows: only looked at."""
+    fwd = [FAKE, 100, 0, 100, 1, FAKE, 32, FAKE, 0, 8, tau, FAKE, FAKE, FAKE, FAKE, 100, None, None]
+    expect = 1 if refused else 0
+    assert q.lib().qlora_distill_topk_fwd(*fwd) == expect
+    assert q.lib().qlora_distill_topk_bwd(*fwd) == expect
