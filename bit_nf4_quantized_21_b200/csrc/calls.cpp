@@ -104,6 +104,11 @@ int64_t as_int(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw python_error();
   return v;
 }
+bool as_bool(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v != 0;
+}
 double as_double(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -177,6 +182,7 @@ PyObject* layernorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    &rstd = tensor(a[4], "rstd");
   Opt w = tensor_or_none(a[2], "weight"), dX = tensor_or_none(a[5], "dX"), dw = tensor_or_none(a[6], "dweight"),
       db = tensor_or_none(a[7], "dbias"), ws = tensor_or_none(a[10], "workspace"), st = tensor_or_none(a[11], "d_status");
+  const bool want_params = as_bool(a[9]);
   const Device d(dY);
   for (Opt t : {&X, &mean, &rstd, w, dX, dw, db, ws, st}) d.same(t);
   const c10::cuda::CUDAGuard guard(d.dev);
@@ -188,7 +194,7 @@ PyObject* layernorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     "dY and dX have X's type");
   at::Tensor own_dx, own_dw, own_db, own_ws;
   if (!dX) { own_dx = empty({x.rows, x.cols}, X, X.scalar_type()); dX = &own_dx; }
-  if (PyObject_IsTrue(a[9])) {
+  if (want_params) {
     TORCH_CHECK_TYPE(THPDtype_Check(a[8]), "grad_dtype must be a dtype");
     const at::ScalarType gt = dw   ? dw->scalar_type()
                               : db ? db->scalar_type()
@@ -270,7 +276,7 @@ PyObject* fp8_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* fp8_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   arguments(n, 15);
-  const bool bwd = PyObject_IsTrue(a[0]) != 0;
+  const bool bwd = as_bool(a[0]);
   Opt X = tensor_or_none(a[1], "activations"), out = tensor_or_none(a[12], "output"), st = tensor_or_none(a[14], "d_status");
   if (a[2] != Py_None) fp8_codes(a[5]);
   const Device d(fp8_codes(a[10]));

@@ -112,3 +112,14 @@ def test_temperatures_whose_square_is_no_normal_number_are_refused(tau, refused)
     expect = 1 if refused else 0
     assert q.lib().qlora_distill_topk_fwd(*fwd) == expect
     assert q.lib().qlora_distill_topk_bwd(*fwd) == expect
+
+
+# ------------------------------------------------------------------ truth values
+
+def test_a_flag_without_a_truth_value_raises_its_own_error():
+    class Neither:
+        def __bool__(self):
+            raise OverflowError("neither")
+    x, s = torch.zeros(4, 64), torch.zeros(4)
+    with pytest.raises(OverflowError, match="neither"):
+        q.qlora_layernorm_bwd(x, x, None, s, s, want_params=Neither())
