@@ -447,7 +447,7 @@ struct Fp8GemmArgs {
   void* out;
   int64_t ldo;
   int out_f32;
-  int tma_out;           // tm_out maps the output (16-byte aligned rows)
+  int tma_out;           // tm_out maps the output (rows that start and end on 16 bytes)
   int tiles_m, tiles_n;
   int after_quant;       // launched as a dependent of the quantiser
   int* status;
@@ -758,7 +758,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       if (!live) break;
       // Out through shared memory, 128 bytes of each of the warp's 32 rows at
       // a time (128-byte swizzle), so that global memory sees whole rows of a
-      // box: by a TMA store, or by the lanes where rows are not 16-byte aligned.
+      // box: by a TMA store, or by the lanes where rows do not start and end on
+      // 16 bytes.
       const int per = args.out_f32 ? 32 : 64;                      // columns of a box
 #pragma unroll
       for (int b = 0; b < 2 * HALVES; ++b) {
