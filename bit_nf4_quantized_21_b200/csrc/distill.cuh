@@ -165,7 +165,7 @@ template <typename T, bool FWD>
 __global__ void __launch_bounds__(kDiThreads, 4) k_distill(const DistillArgs a) {
   constexpr int N = DiVec<T>::N;
   __shared__ __align__(16) int s_id[kDiMaxTop];     // vocabulary index, or -1
-  __shared__ float s_t[kDiMaxTop];                  // t, then (t - the largest) / tau
+  __shared__ float s_t[kDiMaxTop];                  // t, then t - the largest
   __shared__ float s_p[kDiMaxTop];                  // p
   __shared__ float s_z[kDiMaxTop];                  // the student's logit at the entry
   __shared__ float2 red[kDiWarps];                  // the warps' (max, sum)
@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(kDiThreads, 4) k_distill(const DistillArgs a) 
     tmax = di_warp_max(tmax);
     const float tref = tmax == -INFINITY ? 0.0f : tmax;
     for (int j = lane; j < a.top; j += 32) {
-      const float d = (s_t[j] - tref) / a.tau;       // (t / tau first would overflow for the type's lowest and highest values)
-      const float e = s_id[j] >= 0 ? expf(d) : 0.0f;
+      const float d = s_t[j] - tref;                 // (t / tau first would overflow for the type's lowest and highest values)
+      const float e = s_id[j] >= 0 ? expf(d / a.tau) : 0.0f;
       s_t[j] = d;
       s_p[j] = e;
       tsum += e;
@@ -315,12 +315,14 @@ __global__ void __launch_bounds__(kDiThreads, 4) k_distill(const DistillArgs a) 
       float kl = 0.0f;
       for (int j = lane; j < a.top; j += 32) {
         const float p = s_p[j];
-        // p = 0 contributes nothing even where q = 0; a NaN p stays
-        if (!(p == 0.0f)) kl += p * ((s_t[j] - tlog) - ((s_z[j] - ref) / a.tau - zlog));
+        // p = 0 contributes nothing even where q = 0; a NaN p stays.  The sum is
+        // of tau / 2 times p (log p - log q): divided by tau, or added up whole,
+        // student logits of the type's lowest value overflow where the loss does not
+        if (!(p == 0.0f)) kl += 0.5f * p * ((s_t[j] - (s_z[j] - ref)) + a.tau * (zlog - tlog));
       }
       kl = di_warp_sum(kl);
       if (lane == 0) {
-        const float f = weight * (a.tau * a.tau);
+        const float f = weight * a.tau * 2.0f;
         a.loss[row] = (s_empty || weight == 0.0f) ? 0.0f : f * kl;
         if (a.lse) a.lse[row] = ref / a.tau + zlog;
       }
