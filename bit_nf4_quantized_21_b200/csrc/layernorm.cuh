@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(ln_bwd_block<GROUP>(), PER > 8 ? 3 : GROUP <= 
 // Many rows of 16-byte aligned chunks: a block walks its rows, which arrive in
 // a ring in shared memory by bulk copies (one thread asks for a whole row),
 // several rows ahead.  Registers alone kept 16 to 32 KB per SM on their way
-// and reached 3 TB/s; the ring keeps about 100 KB.  A slot is refilled after
+// and reached 3 TB/s; the ring keeps up to 200 KB.  A slot is refilled after
 // the block barrier of its row's first reduction, which every thread reaches
 // with the row in registers.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -663,8 +663,9 @@ __global__ void __launch_bounds__(GROUP) k_ln_bwd_ring(const LnArgs a) {
   }
 }
 
-// Any row length: dx with a block per row, then the columns' partials with a
-// thread per column and a run of rows per block row of the grid.
+// Any row length: the columns' partials (k_ln_bwd_cols: a thread per column
+// and a run of rows per block row of the grid), then dx with a block per row.
+// In that order, because dX may be X or dY.
 template <typename T>
 __global__ void __launch_bounds__(kLnStreamThreads) k_ln_bwd_stream(const LnArgs a) {
   __shared__ __align__(16) float2 red[2][32];

@@ -691,7 +691,8 @@ def qlora_distill_topk_bwd(Z: torch.Tensor, ids: torch.Tensor, t: torch.Tensor, 
                            row_weight: torch.Tensor | None = None, grad_loss: torch.Tensor | None = None,
                            dZ: torch.Tensor | None = None, d_status: torch.Tensor | None = None,
                            stream=None) -> torch.Tensor:
-    """The gradient of the losses (weighted by grad_loss) with respect to Z, from the forward's lse."""
+    """The gradient of the losses (weighted by grad_loss) with respect to Z, from the forward's lse: as
+    accurate as lse is in fp32, which a row masked whole by a finite value is not (see qlora_distill_topk_bwd)."""
     if stream is not None:
         with _stream_of(stream, Z):
             return qlora_distill_topk_bwd(Z, ids, t, tau, lse, row_weight, grad_loss, dZ, d_status)

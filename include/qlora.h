@@ -462,7 +462,12 @@ qlora_status qlora_layernorm_bwd(const void* dY, int64_t lddy, const void* X, in
  *   it receives the gradient for g = 1 in the same launch, so that the
  *   logits are read from memory once.  dZ may be Z (same stride), otherwise
  *   they may not overlap.
- * bwd: the gradient from the saved lse.  dZ may be Z (same stride).
+ * bwd: the gradient with q_v = exp(z_v / tau - lse_i) from the saved lse.  dZ
+ *   may be Z (same stride).  q is as good as an fp32 lse: off by 2^-24 |lse|
+ *   relative.  A row that holds nothing but its type's lowest value (masked
+ *   whole by a finite number) is beyond that: -3e38 + log(vocab) is -3e38, so
+ *   each q comes out as 1, where the gradient of fwd has 1 / vocab.  Give
+ *   such a row the weight 0, or take the gradient from fwd.
  * rows = 0 is a no-op.  fp32 arithmetic; the gradient is rounded once.
  * Deterministic.
  */
