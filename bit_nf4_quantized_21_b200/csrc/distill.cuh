@@ -16,11 +16,11 @@
 // The maximum is subtracted before the scale is applied, the student's and the
 // teacher's alike, so logits masked with the type's lowest value neither
 // overflow nor, where a row or a list holds nothing else, make anything but a
-// uniform softmax.  The gradient is a second sweep over
-// the row, which by then sits in L2 (rows in flight: a few per SM, tens of
-// MB in 126 MB), so a call that returns both reads the logits from memory
-// once.  Bound: HBM (one read, and one write of the gradient), closely
-// followed by the special-function unit, 16 exponentials per clock per SM.
+// uniform softmax.  The gradient is a second sweep over the row, which by then
+// sits in L2 (rows in flight: a few per SM, tens of MB in 126 MB), so a call
+// that returns both reads the logits from memory once.  Bound: HBM (one read,
+// and one write of the gradient), closely followed by the special-function
+// unit, 16 exponentials per clock per SM.
 //
 // A row belongs to a cluster of CTAs, each sweeping a slice of the
 // vocabulary: one CTA when there are rows enough to fill the GPU, up to
@@ -31,10 +31,12 @@
 // a short row's time.  Rows may start at any element: the vector part of a row runs
 // from its first 16-byte boundary, the ragged ends element by element.
 //
-// Measured, against a copy's rate of 6.57 TB/s: loss and gradient in one call
-// 4096 x 32768 bf16 104 us (5.2 TB/s; the copy would take 82), fp32 204 us
-// (164), 1024 x 131072 bf16 120 us (82); loss alone 4096 x 32768 bf16 55 us
-// (41), 6 x 131072 5.2 us; gradient alone 777 x 50021 fp32 59 us (47).
+// Measured on the device (calls in a graph, each on inputs that are not in L2)
+// against a copy's rate of 6.57 TB/s: loss and gradient in one call 4096 x
+// 32768 bf16 108 us (5.0 TB/s; the copy would take 82), fp32 207 us (163),
+// 1024 x 131072 bf16 124 us (82); loss alone 4096 x 32768 bf16 56 us (41),
+// fp32 88 us (82), 6 x 131072 5.1 us; gradient alone 4096 x 32768 bf16 91 us
+// (82), fp32 177 us (163), 777 x 50021 bf16 34.5 us (24), fp32 61 us (47).
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>

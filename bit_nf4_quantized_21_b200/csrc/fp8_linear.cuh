@@ -31,12 +31,19 @@
 // serve both directions: a tile of 128 rows x 128 bytes is a K-major operand
 // forward and an MN-major one in dX.  Where there are few tiles they are 128
 // columns wide, a whole block to an accumulator, three in flight.
-//   Measured with the quantiser ahead of it: 2048 x 11008 x 4096 forward 91
-// us (2.02 PFLOP/s), dX 99 us; 1000 x 4100 x 4040 27 us; 64 x 4096 x 4096 16
-// us.  What bounds it now is the epilogue warps' way for a half of a block:
-// notice that it is there, take 64 columns out (one warp in a quarter of the
-// tensor memory at a time), hand the place back, 32 packed multiply-adds;
-// 0.24 us, where the MMAs need 0.14.
+//   Measured on the device (calls in a graph, each on inputs that are not in
+// L2, the quantiser ahead of the product): 2048 x 11008 x 4096 forward 90 us
+// (2.05 PFLOP/s; 85 without the quantiser, 97 with fp32 in and out), dX 99 us;
+// one after the other from the public entry, where power and launches count,
+// 108 (1.71 PFLOP/s) and 116.  1000 x 4100 x 4040 28.6 us (N = 4096, whose rows
+// TMA can write: 25.7).  Fewer tokens leave most pairs idle while each walks
+// its contraction alone: 64 x 4096 x 4096 16.6 us (its bytes: 2.7), 256 x
+// 11008 x 4096 22.8 (8.0), dX of 1 to 64 tokens x 28672 x 512 73 (2.2) and
+// x 28672 x 8192 77 to 113 (36).
+//   With many tokens, what bounds it now is the epilogue warps' way for a half
+// of a block: notice that it is there, take 64 columns out (one warp in a
+// quarter of the tensor memory at a time), hand the place back, 32 packed
+// multiply-adds; 0.24 us, where the MMAs need 0.14.
 //
 // k_fp8_gemv (few tokens, forward), HBM bound: the weight streams once from
 // global memory straight into the registers of legacy warp-level MMAs
@@ -45,9 +52,12 @@
 // whole 64-byte pieces of its rows.  The tokens' codes sit in shared memory.
 // Behind the quantiser the kernel is a programmatic dependent launch: its
 // first weights travel while the activations are quantised.
-//   Measured with the quantiser: 1 x 28672 x 8192 43 us (5.5 TB/s of weight, a
-// copy's rate is 6.57), 8 x 28672 x 8192 45 us, 7 x 4096 x 4096 8.4 us (two
-// launches and a CTA's one round over its rows).
+//   Measured the same way: 1 x 28672 x 8192 43 us (5.5 TB/s of weight, a
+// copy's rate is 6.57), 8 x 28672 x 8192 45.5 us; 16 tokens 66, 23 tokens 116
+// (fewer blocks on their way as fragments of more tokens fill the registers;
+// from 24 on their codes pass shared memory at this width and the other kernel
+// takes 62).  7 x 4096 x 4096 8.2 us (two launches and a CTA's one round over
+// its rows).
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -119,7 +129,9 @@ __device__ __forceinline__ void f8_load8(const T* row, int64_t c, int64_t cols, 
 }
 
 // Blocks of 1 x 128: sixteen lanes per block, eight elements each.  HBM
-// bound (reads 2 or 4 bytes, writes 1 per element).  A CTA takes 16 rows of
+// bound (reads 2 or 4 bytes, writes 1 per element): 2048 x 11008 bf16 20 us
+// (its bytes at the copy's rate: 10.3), 2048 x 4096 9.4 (3.8), fp32 9.7 (6.4).
+// A CTA takes 16 rows of
 // one block column, so that the scales, which go out block-major ([cols /
 // 128][rows], the order in which the GEMM reads them), leave as one run.
 constexpr int kF8QuantThreads = 256;
@@ -154,6 +166,7 @@ __global__ void __launch_bounds__(kF8QuantThreads) k_fp8_quant_rows(const Fp8Qua
 }
 
 // Blocks of 128 x 128: one CTA per block, 64 elements per thread in registers.
+// 11008 x 4096 fp32 41 us (its bytes at the copy's rate: 34), bf16 72 us (21).
 template <typename T>
 __global__ void __launch_bounds__(256) k_fp8_quant_blocks(const Fp8QuantArgs a) {
   __shared__ uint32_t red[8];

@@ -25,13 +25,18 @@
 // written once per block as a row of partials; k_ln_finish adds the partials
 // in a fixed order (no atomics: results do not depend on scheduling).
 //
-// Measured, against a copy's rate of 6.57 TB/s (bf16 unless said): forward
-// 8192 x 8192 47.3 us (5.7 TB/s; the copy would take 40.9), 4096 x 4096 12.2
-// us, 16 x 4096 3.0 us (two dependent trips to memory and a launch).
-// Backward 8192 x 8192 74 us (61.3), 4096 x 4096 24.2 us (15.3; 18.0 without
-// the parameters' gradients: writing one row of partials per block and adding
-// them up is the rest), 1237 x 2051 fp32 14.4 us (4.6; single-element loads,
-// three rows per SM).
+// Measured on the device (calls in a graph, each on inputs that are not in L2)
+// against a copy's rate of 6.57 TB/s, bf16 unless said.  Forward 8192 x 8192
+// 48 us (5.6 TB/s; the copy would take 40.9), 4096 x 4096 16.8 us (10.2), fp32
+// 26 us (20.4), 16 x 4096 2.9 us (two dependent trips to memory and a launch).
+// Backward 8192 x 8192 77 us (61.3), 4096 x 4096 26 us (15.3; 21.7 without the
+// parameters' gradients: writing one row of partials per block and adding them
+// up is the rest), fp32 40 us (30.7).  Rows that are not 16-byte aligned take
+// single-element loads and stores and never the ring: 8000 x 1500 bf16 31 us
+// forward (7.3) and 56 backward (11.0), 1237 x 2051 fp32 19 us backward (4.6).
+// The streaming kernels: 4096 x 12288 fp32 88 us forward (61) and 262 backward
+// (92; 149 without the parameters' gradients), 2048 x 12001 bf16 50 (15) and
+// 120 (22).
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>

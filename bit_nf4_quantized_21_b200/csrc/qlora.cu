@@ -1354,8 +1354,8 @@ bool ensure_fp8_attrs() {
   });
 }
 
-// Up to this many tokens, and as long as their codes fit in shared memory,
-// the forward takes the weight-streaming kernel.
+// Up to this many tokens, and as long as their codes fit in shared memory (23
+// tokens at K = 8192), the forward takes the weight-streaming kernel.
 constexpr int64_t kF8GemvMaxM = 32;
 int fp8_gemv_nt(int64_t M) { return M <= 8 ? 1 : M <= 16 ? 2 : 4; }
 bool fp8_takes_gemv(int64_t M, int64_t K) {
